@@ -10,6 +10,11 @@
  *   kaio_gemm_f16f32_bwd    its backward: f16 gradients of A and B
  *                           (kaio_gemm_f16f32_bwd_noalloc: the same without a workspace)
  *   kaio_dequant_group_bwd  straight-through per-group dequant backward
+ *   kaio_linear_w4a16       W4A16 product with bias, activation and residual
+ *   kaio_rope_append        rotary positions on Q and K, K and V written to a
+ *                           paged cache
+ *   kaio_paged_attention    attention of new tokens over that cache (with a
+ *                           second launch where the keys of a row are split)
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -242,6 +247,139 @@ kaio_status kaio_dequant_group_bwd(kaio_dtype dtype, int32_t outer, int32_t axis
  * 8, or a null plan -> INVALID_ARGUMENT; k % 128 != 0 -> INVALID_PROBLEM.
  */
 kaio_status kaio_qkv_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t bits, uint32_t plan[5]);
+
+/* Activations of kaio_linear_w4a16's epilogue. */
+typedef enum kaio_activation {
+  KAIO_ACT_NONE = 0,
+  KAIO_ACT_RELU = 1,      /* max(y, 0), NaN kept                                      */
+  KAIO_ACT_GELU = 2,      /* y (1 + erf(y / sqrt 2)) / 2                              */
+  KAIO_ACT_GELU_TANH = 3, /* y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2        */
+  KAIO_ACT_SILU = 4       /* y / (1 + exp(-y))                                        */
+} kaio_activation;
+
+/*
+ * W4A16 product with an epilogue, the projection after attention and the
+ * products of a feed-forward block on the same packed weights as the QKV
+ * projection:
+ *
+ *   y[m, n] = act( sum_k x[m, k] * int4(W, k, n) * S[k / 128, n] + b[n] ) + r[m, n]
+ *
+ *   x  f16[m, k]   w  u32[k/8, n] and s  f16[k/128, n] as kaio_qkv_w4a16
+ *   bias      f16[n] or NULL        residual  f16[m, n] or NULL
+ *   y         f16[m, n]; may be the residual's buffer itself (updated in place)
+ *   group_size  must be 128
+ *
+ * The sum, the bias, the activation and the residual are in f32, rounded once
+ * to f16 (RNE).
+ *
+ * Validation order: group_size != 128 -> UNSUPPORTED; unknown activation ->
+ * UNSUPPORTED; k % 128 != 0 -> INVALID_PROBLEM; m == 0 or n == 0 -> OK
+ * (nothing launched); too large (limits of kaio_qkv_w4a16) ->
+ * INVALID_PROBLEM; null pointer (x, w and s only when k > 0) ->
+ * INVALID_ARGUMENT; misaligned (16 bytes) -> INVALID_ARGUMENT; y overlapping
+ * an input (other than residual == y) -> INVALID_ARGUMENT; device -> DEVICE;
+ * launch -> LAUNCH.  k == 0: the product is zero, the epilogue still runs.
+ */
+kaio_status kaio_linear_w4a16(const void* x, const uint32_t* w, const void* s,
+                              const void* bias, const void* residual, void* y,
+                              uint32_t m, uint32_t n, uint32_t k, uint32_t group_size,
+                              kaio_activation activation, void* stream);
+
+/*
+ * A paged key/value cache and the batch that uses it.  The struct itself is in
+ * host memory and read during the call; the pointers are device pointers.
+ *
+ * Sequence s has the new tokens of rows q_start[s] .. q_start[s+1]-1 and
+ * lens[s] tokens in the cache with the new ones last: row t of it is at
+ * position lens[s] - (q_start[s+1] - t).  The token at position c lies in slot
+ * c % page_size of page page_table[s][c / page_size].
+ *
+ * The contents of page_table, q_start and lens are read on the device and may
+ * change from call to call (a captured graph sees them at replay).  A page id
+ * outside [0, pages), -1 by custom, is a page that is not there: a released
+ * page or one not needed yet.  Its positions are not visible, and nothing is
+ * written to it; so are positions past table_width * page_size.  Rows of q in
+ * no sequence (a batch padded past q_start[seqs]) see nothing.
+ * Calls read and write the cache only through present pages.  No two
+ * sequences may write to one page.
+ */
+typedef struct kaio_paged_kv {
+  void* k_cache;              /* [pages, page_size, kv_heads, head_dim] */
+  void* v_cache;              /* the same shape                         */
+  const int32_t* page_table;  /* [seqs, table_width]                    */
+  const int32_t* q_start;     /* [seqs + 1], ascending                  */
+  const int32_t* lens;        /* [seqs]                                 */
+  int32_t dtype;              /* KAIO_DTYPE_F16 or KAIO_DTYPE_BF16: cache and q, k, v, outputs */
+  uint32_t pages, page_size, kv_heads, head_dim;
+  uint32_t seqs, table_width;
+} kaio_paged_kv;
+
+/*
+ * Rotary positions on Q and K, K and V written to the paged cache.
+ *
+ * Pair j < half of every head of q and k (elements 2j and 2j+1 when
+ * interleaved, else j and j + half) is turned by the angle
+ * a = positions[axis(j)][t] * inv_freq[j], taken in 64 bits:
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a)
+ * in f32, rounded once.  sections[i] consecutive pairs belong to axis i; half
+ * is their sum.  Elements past 2 * half pass through.  The turned K and V of
+ * row t go to the slot of its position.
+ *
+ *   q  [tokens, q_heads, head_dim]   k, v  [tokens, kv_heads, head_dim]
+ *   positions  i32[axes, tokens]     inv_freq  f64[half]
+ *   sections   u32[axes], in HOST memory
+ *   q_out      as q; may be q itself (turned in place)
+ *
+ * Validation order: kv null -> INVALID_ARGUMENT; dtype -> UNSUPPORTED; axes
+ * not in [1, 8], head_dim > 1024 -> UNSUPPORTED; page_size, kv_heads or
+ * head_dim zero, 2 * half > head_dim -> INVALID_PROBLEM; tokens == 0 -> OK
+ * (nothing launched); too large (2^31 slots, 2^24 - 1 workgroups, 2^62 bytes)
+ * -> INVALID_PROBLEM; null, misaligned (16 bytes; integers and inv_freq by
+ * element) or overlapping pointer -> INVALID_ARGUMENT; device -> DEVICE;
+ * launch -> LAUNCH.
+ */
+kaio_status kaio_rope_append(const kaio_paged_kv* kv, const void* q, const void* k, const void* v,
+                             const int32_t* positions, const double* inv_freq,
+                             const uint32_t* sections, uint32_t axes, int32_t interleaved,
+                             void* q_out, uint32_t tokens, uint32_t q_heads, void* stream);
+
+/*
+ * Attention of the new tokens over the paged cache: decode, chunks of prompts
+ * and whole prompts, causal, with grouped heads (q head h reads K/V head
+ * h / (q_heads / kv_heads)).
+ *
+ *   out[t, h] = sum_c softmax_c(scale * q[t, h] . K[c]) V[c]
+ *
+ * over the visible positions c of the row at position pos: c <= pos, c <
+ * lens[s], its page there, and, with window > 0, c > pos - window or c < sinks.
+ * A row that sees nothing is zero.  Scores, softmax and sums are f32.
+ * Invisible positions are not read into the result, whatever they hold.
+ *
+ *   q, out  [tokens, q_heads, head_dim]
+ *   max_new    the most new tokens a sequence has (it chooses the kernel; a
+ *              larger number in q_start is still served correctly)
+ *   window     0: none                sinks  first tokens that stay visible
+ *   workspace  device scratch of at least kaio_paged_attention_workspace_size
+ *              bytes, 16-byte aligned (NULL when that is 0); unspecified on
+ *              return.  Calls on one workspace must not overlap in time.
+ *
+ * Results are deterministic for given sizes and contents of lens and q_start.
+ *
+ * Validation order: kv null -> INVALID_ARGUMENT; dtype -> UNSUPPORTED;
+ * page_size, kv_heads or head_dim zero, q_heads not a multiple of kv_heads,
+ * scale not finite -> INVALID_PROBLEM; head_dim > 256 -> UNSUPPORTED; tokens
+ * == 0 or q_heads == 0 -> OK; max_new == 0 or too large -> INVALID_PROBLEM; null,
+ * misaligned or overlapping pointer, workspace too small ->
+ * INVALID_ARGUMENT; device -> DEVICE; launch -> LAUNCH.
+ */
+kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* out,
+                                 uint32_t tokens, uint32_t q_heads, uint32_t max_new,
+                                 float scale, uint32_t window, uint32_t sinks,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes kaio_paged_attention needs for these sizes (0 for sizes it refuses). */
+size_t kaio_paged_attention_workspace_size(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads,
+                                           uint32_t max_new);
 
 /* Message of the calling thread's most recent failed call ("" after a success). */
 const char* kaio_last_error(void);

@@ -11,6 +11,10 @@ device is not gfx950 the call raises.
     kaio_gemm_f16f32(a, b) -> c
     kaio_gemm_f16f32_bwd(a, b, grad) -> (grad_a, grad_b)
     kaio_dequant_group_bwd(dy, scale, group_size) -> dq
+    kaio_linear_w4a16(x, w, s, bias=, activation=, residual=) -> y
+    KaioPagedKV(k_cache, v_cache, page_table, q_start, lens): a paged cache and its batch, for
+    kaio_rope_append(q, k, v, positions, inv_freq, sections, paged) -> q
+    kaio_paged_attention(q, paged, max_new, scale, window=, sinks=) -> out
 """
 from __future__ import annotations
 
@@ -18,7 +22,8 @@ import ctypes
 import os
 
 __all__ = ["DTYPE_CODES", "KaioError", "kaio_qkv_w4a16", "kaio_qkv_w8a16", "kaio_gemm_f16f32", "kaio_gemm_f16f32_bwd",
-           "kaio_dequant_group_bwd",
+           "kaio_dequant_group_bwd", "kaio_linear_w4a16", "KaioPagedKV", "kaio_rope_append", "kaio_paged_attention",
+           "ACTIVATION_CODES",
            "kaio_last_error", "kaio_version", "lib", "LIB_PATH", "GROUP_SIZE"]
 
 # KAIO_LIBRARY may name another in-tree build of the same library (the host-sanitizer
@@ -28,6 +33,7 @@ GROUP_SIZE = 128
 
 STATUS = {0: "OK", 1: "INVALID_ARGUMENT", 2: "INVALID_PROBLEM", 3: "UNSUPPORTED", 4: "DEVICE", 5: "LAUNCH"}
 DTYPE_CODES = {"f32": 0, "bf16": 1, "f16": 2, "f64": 3}
+ACTIVATION_CODES = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class KaioError(RuntimeError):
@@ -38,6 +44,13 @@ class KaioError(RuntimeError):
 
 
 _lib = None
+
+
+class _PagedKV(ctypes.Structure):
+    """kaio_paged_kv of include/kaio.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "page_table", "q_start", "lens")] + \
+               [("dtype", ctypes.c_int32)] + \
+               [(n, ctypes.c_uint32) for n in ("pages", "page_size", "kv_heads", "head_dim", "seqs", "table_width")]
 
 
 def lib() -> ctypes.CDLL:
@@ -65,6 +78,14 @@ def lib() -> ctypes.CDLL:
         L.kaio_dequant_group_bwd.restype = ctypes.c_int
         L.kaio_qkv_plan.argtypes = [u32] * 4 + [vp]
         L.kaio_qkv_plan.restype = ctypes.c_int
+        L.kaio_linear_w4a16.argtypes = [vp] * 6 + [u32] * 4 + [ctypes.c_int, vp]
+        L.kaio_linear_w4a16.restype = ctypes.c_int
+        L.kaio_rope_append.argtypes = [vp] * 7 + [u32, i32, vp, u32, u32, vp]
+        L.kaio_rope_append.restype = ctypes.c_int
+        L.kaio_paged_attention.argtypes = [vp] * 3 + [u32] * 3 + [ctypes.c_float, u32, u32, vp, ctypes.c_size_t, vp]
+        L.kaio_paged_attention.restype = ctypes.c_int
+        L.kaio_paged_attention_workspace_size.argtypes = [vp, u32, u32, u32]
+        L.kaio_paged_attention_workspace_size.restype = ctypes.c_size_t
         L.kaio_last_error.argtypes = []
         L.kaio_last_error.restype = ctypes.c_char_p
         L.kaio_version.argtypes = []
@@ -101,7 +122,7 @@ def _stream(device, stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _tensor(t, name, dtypes, device=None, rank=2):
+def _tensor(t, name, dtypes, device=None, rank=2, any_offset=False):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -113,8 +134,8 @@ def _tensor(t, name, dtypes, device=None, rank=2):
         raise ValueError(f"{name} must be on a HIP device; there is no CPU fallback")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous() or t.storage_offset() != 0:
-        raise ValueError(f"{name} must be contiguous with zero offset")
+    if not t.is_contiguous() or (t.storage_offset() != 0 and not any_offset):
+        raise ValueError(f"{name} must be contiguous" + ("" if any_offset else " with zero offset"))
     return t
 
 
@@ -248,3 +269,166 @@ def kaio_dequant_group_bwd(dy, scale, group_size, dq=None, stream=None):
     _check(lib().kaio_dequant_group_bwd(codes[dy.dtype], outer, axis, group_size, dy.data_ptr(),
                                         scale.data_ptr(), dq.data_ptr(), None, 0, _stream(dy.device, stream)))
     return dq
+
+
+def kaio_linear_w4a16(x, w, s, bias=None, activation="none", residual=None, y=None, stream=None):
+    """y = act(x . (int4(w) * s) + bias) + residual, one rounding to f16; returns y f16[M, N].
+
+    x f16[M,K]; w packed INT4 as int32/uint32 [K/8, N]; s f16[K/128, N]; bias f16[N]; residual f16[M, N];
+    activation one of ACTIVATION_CODES.  ``y`` may be ``residual`` itself (updated in place).
+    """
+    import torch
+    f16 = (torch.float16,)
+    _tensor(x, "x", f16, any_offset=True)
+    dev = x.device
+    _tensor(w, "w_packed", _u32_dtypes(), dev, any_offset=True)
+    _tensor(s, "scales", f16, dev, any_offset=True)
+    M, K = x.shape
+    N = w.shape[1]
+    if K % GROUP_SIZE:
+        raise ValueError(f"K ({K}) must be a multiple of group_size ({GROUP_SIZE})")
+    if w.shape[0] != K // 8:
+        raise ValueError(f"w_packed has {w.shape[0]} rows, expected K/8 = {K // 8} (K={K})")
+    if tuple(s.shape) != (K // GROUP_SIZE, N):
+        raise ValueError(f"scales must be [{K // GROUP_SIZE}, {N}], got {list(s.shape)}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}: one of {tuple(ACTIVATION_CODES)}")
+    if bias is not None:
+        _tensor(bias, "bias", f16, dev, rank=1, any_offset=True)
+        if bias.shape[0] != N:
+            raise ValueError(f"bias must be [{N}], got {list(bias.shape)}")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float16, device=dev)
+    for t, n in ((residual, "residual"), (y, "y")):
+        if t is not None:
+            _tensor(t, n, f16, dev, any_offset=True)
+            if tuple(t.shape) != (M, N):
+                raise ValueError(f"{n} must be [{M}, {N}], got {list(t.shape)}")
+    for dim in (M, N, K):
+        if dim >= 2 ** 32:
+            raise ValueError("dimension exceeds u32")
+    _check(lib().kaio_linear_w4a16(x.data_ptr(), w.data_ptr(), s.data_ptr(),
+                                   None if bias is None else bias.data_ptr(),
+                                   None if residual is None else residual.data_ptr(), y.data_ptr(),
+                                   M, N, K, GROUP_SIZE, ACTIVATION_CODES[activation], _stream(dev, stream)))
+    return y
+
+
+class KaioPagedKV:
+    """A paged key/value cache and the batch that uses it (kaio_paged_kv of include/kaio.h).
+
+    k_cache, v_cache  f16 or bf16 [pages, page_size, kv_heads, head_dim]
+    page_table        int32 [seqs, width]; an id outside [0, pages), -1 by custom, is a page that is not there
+    q_start           int32 [seqs + 1], ascending: rows of q of each sequence's new tokens
+    lens              int32 [seqs]: tokens of each sequence, the new ones last
+
+    Holds the tensors; made once and kept while they live, as only their addresses and shapes are taken here.
+    What page_table, q_start and lens hold is read on the device by each call.
+    """
+
+    def __init__(self, k_cache, v_cache, page_table, q_start, lens):
+        import torch
+        _tensor(k_cache, "k_cache", (torch.float16, torch.bfloat16), rank=4, any_offset=True)
+        dev = k_cache.device
+        _tensor(v_cache, "v_cache", (k_cache.dtype,), dev, rank=4, any_offset=True)
+        if v_cache.shape != k_cache.shape:
+            raise ValueError(f"v_cache must be {list(k_cache.shape)}, got {list(v_cache.shape)}")
+        i32 = (torch.int32,)
+        _tensor(page_table, "page_table", i32, dev, any_offset=True)
+        _tensor(q_start, "q_start", i32, dev, rank=1, any_offset=True)
+        _tensor(lens, "lens", i32, dev, rank=1, any_offset=True)
+        seqs = lens.shape[0]
+        if page_table.shape[0] != seqs or q_start.shape[0] != seqs + 1:
+            raise ValueError(f"page_table has {page_table.shape[0]} rows and q_start {q_start.shape[0]} entries, "
+                             f"expected {seqs} and {seqs + 1}")
+        if max(*k_cache.shape, seqs, page_table.shape[1]) >= 2 ** 31:
+            raise ValueError("dimension exceeds i32")
+        self.k_cache, self.v_cache, self.page_table, self.q_start, self.lens = k_cache, v_cache, page_table, q_start, lens
+        self.device, self.dtype = dev, k_cache.dtype
+        self.pages, self.page_size, self.kv_heads, self.head_dim = k_cache.shape
+        self.seqs = seqs
+        self._c = _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), q_start.data_ptr(),
+                           lens.data_ptr(), 2 if self.dtype == torch.float16 else 1, *k_cache.shape, seqs,
+                           page_table.shape[1])
+        self._ref = ctypes.byref(self._c)
+
+    def _heads(self, t, name, heads=None):
+        _tensor(t, name, (self.dtype,), self.device, rank=3, any_offset=True)
+        if t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
+            raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {self.head_dim}], "
+                             f"got {list(t.shape)}")
+        return t
+
+
+def _paged(paged):
+    if not isinstance(paged, KaioPagedKV):
+        raise TypeError("paged must be a KaioPagedKV")
+    return paged
+
+
+def kaio_rope_append(q, k, v, positions, inv_freq, sections, paged, interleaved=False, q_out=None, stream=None):
+    """Rotary positions on q and k, k and v written to the paged cache; returns the turned q.
+
+    q [T, q_heads, head_dim], k and v [T, kv_heads, head_dim] in the cache's dtype; positions int32 [axes, T];
+    inv_freq float64 [pairs]; sections: how many consecutive pairs each axis turns (their sum is ``pairs``;
+    elements past 2 * pairs of a head pass through).  Pair j is elements (2j, 2j+1) when ``interleaved``, else
+    (j, j + pairs).  ``q_out`` may be ``q`` itself (turned in place).
+    """
+    import torch
+    p = _paged(paged)
+    p._heads(q, "q")
+    T = q.shape[0]
+    p._heads(k, "k", p.kv_heads)
+    p._heads(v, "v", p.kv_heads)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"k and v must have q's {T} rows, got {k.shape[0]} and {v.shape[0]}")
+    _tensor(positions, "positions", (torch.int32,), p.device, any_offset=True)
+    _tensor(inv_freq, "inv_freq", (torch.float64,), p.device, rank=1, any_offset=True)
+    axes = len(sections)
+    if tuple(positions.shape) != (axes, T):
+        raise ValueError(f"positions must be [{axes}, {T}], got {list(positions.shape)}")
+    if min(sections, default=0) < 0 or sum(sections) != inv_freq.shape[0]:
+        raise ValueError(f"sections {list(sections)} must be counts that add up to the {inv_freq.shape[0]} pairs of inv_freq")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    p._heads(q_out, "q_out")
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
+    if T >= 2 ** 31 or q.shape[1] >= 2 ** 31:
+        raise ValueError("dimension exceeds i32")
+    _check(lib().kaio_rope_append(p._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
+                                  inv_freq.data_ptr(), (ctypes.c_uint32 * axes)(*sections), axes, int(bool(interleaved)),
+                                  q_out.data_ptr(), T, q.shape[1], _stream(p.device, stream)))
+    return q_out
+
+
+def kaio_paged_attention(q, paged, max_new, scale, window=0, sinks=0, out=None, workspace=None, stream=None):
+    """Causal attention of the new tokens over the paged cache; returns out, shaped as q.
+
+    q [T, q_heads, head_dim] in the cache's dtype, q_heads a multiple of the cache's heads; ``max_new``: the most
+    new tokens a sequence has (it chooses the kernel).  With ``window`` > 0 a row at position p sees positions
+    above p - window and the first ``sinks``.  A row that sees nothing is zero.  ``workspace`` (uint8) is
+    allocated here when it is needed and not given.
+    """
+    import torch
+    p = _paged(paged)
+    p._heads(q, "q")
+    T, hq, _ = q.shape
+    if hq % p.kv_heads:
+        raise ValueError(f"q has {hq} heads, not a multiple of the cache's {p.kv_heads}")
+    if out is None:
+        out = torch.empty_like(q)
+    p._heads(out, "out")
+    if out.shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+    if max_new < 0 or window < 0 or sinks < 0 or max(T, hq, max_new, window, sinks) >= 2 ** 31:
+        raise ValueError("max_new, window and sinks must be counts that fit in i32")
+    need = lib().kaio_paged_attention_workspace_size(p._ref, T, hq, max_new)
+    if workspace is None and need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=p.device)
+    if workspace is not None:
+        _tensor(workspace, "workspace", (torch.uint8,), p.device, rank=1, any_offset=True)
+    _check(lib().kaio_paged_attention(p._ref, q.data_ptr(), out.data_ptr(), T, hq, max_new, scale, window, sinks,
+                                      None if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel(), _stream(p.device, stream)))
+    return out

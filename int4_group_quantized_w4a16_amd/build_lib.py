@@ -25,7 +25,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkaio.so")
-SOURCES = ["kaio_abi.cpp", "qkv_prefill.hip", "qkv_decode.hip", "gemm_f16f32.hip", "dequant_group_bwd.hip"]
+SOURCES = ["kaio_abi.cpp", "qkv_prefill.hip", "qkv_decode.hip", "gemm_f16f32.hip", "dequant_group_bwd.hip",
+           "linear_w4a16.hip", "rope_append.hip", "paged_attention.hip"]
 # measurement aid for the benchmark (a plain streaming read), a library of its own
 ROOF_LIB = os.path.join(PKG, "libkaio_roof.so")
 ROOF_SOURCES = ["roof.hip"]

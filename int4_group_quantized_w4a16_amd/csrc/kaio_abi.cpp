@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -244,6 +245,68 @@ kaio_status qkv(const char* op, uint32_t bits, const void* x, const uint32_t* w_
   return launched(op, decode ? kaio::launch_qkv_decode(p, s) : kaio::launch_qkv_prefill(p, s));
 }
 
+bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// an enum parameter's code, read from its bytes (a C caller may pass any int)
+template <typename E>
+int code_of(const E& e) {
+  static_assert(sizeof(E) == sizeof(int), "enums are passed as ints");
+  int code = 0;
+  std::memcpy(&code, &e, sizeof code);
+  return code;
+}
+
+// The checks of a paged cache that need no pointers: dtype and sizes.
+kaio_status check_paged_sizes(const char* op, const kaio_paged_kv* kv) {
+  if (!kv) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "kv is null");
+  if (kv->dtype != KAIO_DTYPE_F16 && kv->dtype != KAIO_DTYPE_BF16)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "unsupported dtype %d (f16, bf16)", kv->dtype);
+  if (kv->page_size == 0 || kv->kv_heads == 0 || kv->head_dim == 0)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "page_size (%u), kv_heads (%u) and head_dim (%u) must be > 0",
+                kv->page_size, kv->kv_heads, kv->head_dim);
+  return KAIO_OK;
+}
+
+bool paged_fits(const kaio_paged_kv* kv, uint64_t* cache_bytes, uint64_t* table_bytes) {
+  const uint64_t slots = (uint64_t)kv->pages * kv->page_size;
+  return slots < (1ull << 31) && (uint64_t)kv->kv_heads * kv->head_dim < (1ull << 31) &&
+         bytes_of(slots, (uint64_t)kv->kv_heads * kv->head_dim, 2, cache_bytes) &&
+         bytes_of(kv->seqs, kv->table_width, 4, table_bytes) && kv->seqs < (1u << 31);
+}
+
+kaio_status check_paged_pointers(const char* op, const kaio_paged_kv* kv) {
+  const bool cache = kv->pages > 0, table = kv->seqs > 0 && kv->table_width > 0;
+  const struct { const void* p; const char* name; bool used; uintptr_t align; } all[5] = {
+      {kv->k_cache, "k_cache", cache, 16}, {kv->v_cache, "v_cache", cache, 16},
+      {kv->page_table, "page_table", table, 4}, {kv->q_start, "q_start", kv->seqs > 0, 4},
+      {kv->lens, "lens", kv->seqs > 0, 4}};
+  for (const auto& a : all)
+    if (a.used && !a.p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is null", a.name);
+  for (const auto& a : all)
+    if (a.used && !aligned_to(a.p, a.align))
+      return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is not %u-byte aligned", a.name, (unsigned)a.align);
+  return KAIO_OK;
+}
+
+kaio::PagedKV paged_of(const kaio_paged_kv* kv, uint32_t tokens) {
+  kaio::PagedKV p;
+  p.k = static_cast<uint16_t*>(kv->k_cache);
+  p.v = static_cast<uint16_t*>(kv->v_cache);
+  p.table = kv->page_table;
+  p.q_start = kv->q_start;
+  p.lens = kv->lens;
+  p.pages = kv->pages;
+  p.kv_heads = kv->kv_heads;
+  p.head_dim = kv->head_dim;
+  p.seqs = kv->seqs;
+  p.width = kv->table_width;
+  const uint64_t cap = (uint64_t)kv->table_width * kv->page_size;
+  p.cap = cap < 0x7FFFFFFFull ? (uint32_t)cap : 0x7FFFFFFFu;
+  p.page = kaio::FastDiv::of(kv->page_size);
+  p.tokens = tokens;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -382,6 +445,175 @@ kaio_status kaio_qkv_plan(uint32_t m, uint32_t n, uint32_t k, uint32_t bits, uin
     plan[4] = wgs > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)wgs;
   }
   return ok();
+}
+
+kaio_status kaio_linear_w4a16(const void* x, const uint32_t* w, const void* s, const void* bias,
+                              const void* residual, void* y, uint32_t m, uint32_t n, uint32_t k,
+                              uint32_t group_size, kaio_activation activation, void* stream) {
+  static const char* op = "linear_w4a16";
+  if (group_size != 128)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "group_size (%u) must be 128 (locked by the kernel contract)", group_size);
+  const int act = code_of(activation);
+  if (act < KAIO_ACT_NONE || act > KAIO_ACT_SILU) return fail(KAIO_ERR_UNSUPPORTED, op, "unknown activation %d", act);
+  if (k % 128 != 0)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "K (%u) must be a multiple of group_size (128)", k);
+  if (m == 0 || n == 0) return ok();
+  uint64_t out_bytes = 0, x_bytes = 0, w_bytes = 0, s_bytes = 0;
+  const uint64_t wgs = kaio::linear_wgs(m, n);
+  if (!bytes_of(m, n, 2, &out_bytes) || !bytes_of(m, k, 2, &x_bytes) || !bytes_of(k / 8, n, 4, &w_bytes) ||
+      !bytes_of(k / 128, n, 2, &s_bytes) || wgs > kaio::kMaxWorkgroups || n >= kaio::kMaxN || k >= kaio::kMaxK)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (m=%u, n=%u, k=%u)", m, n, k);
+  if (!y) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output y is null");
+  const struct { const void* p; const char* name; } ins[5] = {
+      {x, "x"}, {w, "w_packed"}, {s, "scales"}, {bias, "bias"}, {residual, "residual"}};
+  if (k > 0)
+    for (int i = 0; i < 3; ++i)
+      if (!ins[i].p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input %s is null", ins[i].name);
+  if (!aligned16(y)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output y is not 16-byte aligned");
+  for (int i = k > 0 ? 0 : 3; i < 5; ++i)
+    if (!aligned16(ins[i].p)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input %s is not 16-byte aligned", ins[i].name);
+  const Range ro[1] = {range(y, out_bytes, "y")};
+  const Range ri[5] = {range(x, k > 0 ? x_bytes : 0, "x"), range(w, w_bytes, "w_packed"), range(s, s_bytes, "scales"),
+                       range(bias, bias ? (uint64_t)n * 2 : 0, "bias"),
+                       range(residual, residual && residual != y ? out_bytes : 0, "residual")};
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 1, ri, 5, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output %s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  kaio::LinearProblem p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = w;
+  p.s = static_cast<const uint16_t*>(s);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.y = static_cast<uint16_t*>(y);
+  p.m = m; p.n = n; p.k = k;
+  p.act = act;
+  return launched(op, kaio::launch_linear_w4a16(p, static_cast<hipStream_t>(stream)));
+}
+
+kaio_status kaio_rope_append(const kaio_paged_kv* kv, const void* q, const void* k, const void* v,
+                             const int32_t* positions, const double* inv_freq, const uint32_t* sections,
+                             uint32_t axes, int32_t interleaved, void* q_out, uint32_t tokens, uint32_t q_heads,
+                             void* stream) {
+  static const char* op = "rope_append";
+  if (kaio_status st = check_paged_sizes(op, kv)) return st;
+  if (axes < 1 || axes > kaio::kMaxAxes)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "axes (%u) must be 1 to %u", axes, kaio::kMaxAxes);
+  if (kv->head_dim > 1024) return fail(KAIO_ERR_UNSUPPORTED, op, "head_dim (%u) must be at most 1024", kv->head_dim);
+  if (!sections) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "sections is null");
+  uint64_t half = 0;
+  kaio::RopeAppend p;
+  for (uint32_t a = 0; a < kaio::kMaxAxes; ++a) {
+    p.first_pair[a] = (uint32_t)(half > 0xFFFFFFFFull ? 0xFFFFFFFFull : half);
+    if (a < axes) half += sections[a];
+  }
+  if (2 * half > kv->head_dim)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "sections turn %llu pairs: head_dim (%u) has %u",
+                (unsigned long long)half, kv->head_dim, kv->head_dim / 2);
+  if (tokens == 0) return ok();
+  uint64_t cache_bytes = 0, table_bytes = 0, q_bytes = 0, kv_bytes = 0;
+  const uint64_t heads = (uint64_t)q_heads + 2ull * kv->kv_heads;
+  if (!paged_fits(kv, &cache_bytes, &table_bytes) || tokens >= (1u << 31) ||
+      !bytes_of(tokens, (uint64_t)q_heads * kv->head_dim, 2, &q_bytes) ||
+      !bytes_of(tokens, (uint64_t)kv->kv_heads * kv->head_dim, 2, &kv_bytes) ||
+      heads * kv->head_dim >= (1ull << 31) || tokens > kaio::kMaxWorkgroups)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, heads=%llu, slots=%llu)",
+                tokens, (unsigned long long)heads, (unsigned long long)kv->pages * kv->page_size);
+  if (kaio_status st = check_paged_pointers(op, kv)) return st;
+  const struct { const void* p; const char* name; bool used; uintptr_t align; } all[6] = {
+      {q, "input q", q_heads > 0, 16}, {k, "input k", true, 16}, {v, "input v", true, 16},
+      {q_out, "output q_out", q_heads > 0, 16}, {positions, "positions", half > 0, 4}, {inv_freq, "inv_freq", half > 0, 8}};
+  for (const auto& a : all)
+    if (a.used && !a.p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is null", a.name);
+  for (const auto& a : all)
+    if (a.used && !aligned_to(a.p, a.align))
+      return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is not %u-byte aligned", a.name, (unsigned)a.align);
+  const Range ro[3] = {range(q_out, q_bytes, "q_out"), range(kv->k_cache, cache_bytes, "k_cache"),
+                       range(kv->v_cache, cache_bytes, "v_cache")};
+  const Range ri[8] = {range(q, q != q_out ? q_bytes : 0, "q"), range(k, kv_bytes, "k"), range(v, kv_bytes, "v"),
+                       range(positions, half ? (uint64_t)axes * tokens * 4 : 0, "positions"),
+                       range(inv_freq, half * 8, "inv_freq"), range(kv->page_table, table_bytes, "page_table"),
+                       range(kv->q_start, kv->seqs ? ((uint64_t)kv->seqs + 1) * 4 : 0, "q_start"),
+                       range(kv->lens, (uint64_t)kv->seqs * 4, "lens")};
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 3, ri, 8, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output %s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  p.kv = paged_of(kv, tokens);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_new = static_cast<const uint16_t*>(k);
+  p.v_new = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.axes = axes;
+  p.half = (uint32_t)half;
+  p.q_heads = q_heads;
+  p.per_head = kaio::FastDiv::of(kv->head_dim >= 16 ? kv->head_dim / 16 : 1);
+  p.bf16 = kv->dtype == KAIO_DTYPE_BF16;
+  p.interleaved = interleaved != 0;
+  return launched(op, kaio::launch_rope_append(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t kaio_paged_attention_workspace_size(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads,
+                                           uint32_t max_new) {
+  if (!kv || kv->kv_heads == 0 || q_heads % kv->kv_heads != 0 || kv->page_size == 0 || tokens == 0) return 0;
+  return kaio::paged_attention_workspace(kv->kv_heads, q_heads, kv->head_dim, kv->seqs, tokens, max_new);
+}
+
+kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* out, uint32_t tokens, uint32_t q_heads,
+                                 uint32_t max_new, float scale, uint32_t window, uint32_t sinks, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  static const char* op = "paged_attention";
+  if (kaio_status st = check_paged_sizes(op, kv)) return st;
+  if (q_heads % kv->kv_heads != 0)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "q_heads (%u) must be a multiple of kv_heads (%u)", q_heads, kv->kv_heads);
+  if (!std::isfinite(scale)) return fail(KAIO_ERR_INVALID_PROBLEM, op, "scale must be finite");
+  if (kv->head_dim > 256) return fail(KAIO_ERR_UNSUPPORTED, op, "head_dim (%u) must be at most 256", kv->head_dim);
+  if (tokens == 0 || q_heads == 0) return ok();
+  if (max_new == 0) return fail(KAIO_ERR_INVALID_PROBLEM, op, "max_new must be > 0");
+  uint64_t cache_bytes = 0, table_bytes = 0, q_bytes = 0;
+  if (!paged_fits(kv, &cache_bytes, &table_bytes) || (uint64_t)tokens * q_heads > kaio::kMaxWorkgroups ||
+      !bytes_of(tokens, (uint64_t)q_heads * kv->head_dim, 2, &q_bytes))
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, q_heads=%u, slots=%llu)",
+                tokens, q_heads, (unsigned long long)kv->pages * kv->page_size);
+  if (kaio_status st = check_paged_pointers(op, kv)) return st;
+  const uint64_t need = kaio::paged_attention_workspace(kv->kv_heads, q_heads, kv->head_dim, kv->seqs, tokens, max_new);
+  if (!q) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input q is null");
+  if (!out) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output out is null");
+  if (need && !workspace) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace is null");
+  if (workspace_bytes < need)
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace_bytes (%zu) < %llu needed", workspace_bytes,
+                (unsigned long long)need);
+  if (!aligned16(q)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input q is not 16-byte aligned");
+  if (!aligned16(out)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output out is not 16-byte aligned");
+  if (need && !aligned16(workspace)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace is not 16-byte aligned");
+  const Range ro[2] = {range(out, q_bytes, "out"), range(need ? workspace : nullptr, need, "workspace")};
+  const Range ri[6] = {range(q, q_bytes, "q"), range(kv->k_cache, cache_bytes, "k_cache"),
+                       range(kv->v_cache, cache_bytes, "v_cache"), range(kv->page_table, table_bytes, "page_table"),
+                       range(kv->q_start, kv->seqs ? ((uint64_t)kv->seqs + 1) * 4 : 0, "q_start"),
+                       range(kv->lens, (uint64_t)kv->seqs * 4, "lens")};
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 2, ri, 6, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  kaio::PagedAttention p;
+  p.kv = paged_of(kv, tokens);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.workspace = need ? workspace : nullptr;
+  p.q_heads = q_heads;
+  p.group = kaio::FastDiv::of(q_heads / kv->kv_heads);
+  p.max_new = max_new;
+  p.scale = scale;
+  p.window = window;
+  p.sinks = sinks;
+  p.bf16 = kv->dtype == KAIO_DTYPE_BF16;
+  return launched(op, kaio::launch_paged_attention(p, static_cast<hipStream_t>(stream)));
 }
 
 const char* kaio_last_error(void) { return g_last_error.c_str(); }

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/kaio.h"
+#include "paged.hpp"
 
 namespace kaio {
 
@@ -139,6 +140,49 @@ hipError_t launch_gemm_f16f32_bwd_noalloc(const uint16_t* a, const uint16_t* b, 
                                           uint32_t k, hipStream_t stream);
 hipError_t launch_gemm_f16f32(const uint16_t* a, const uint16_t* b, float* c,
                               uint32_t m, uint32_t n, uint32_t k, hipStream_t stream);
+// y = act(x . (int4(W) * S) + bias) + residual; bias and residual may be null.
+struct LinearProblem {
+  const uint16_t* x;          // f16 [m, k]
+  const uint32_t* w;          // u32 [k / 8, n]
+  const uint16_t* s;          // f16 [k / 128, n]
+  const uint16_t* bias;       // f16 [n]
+  const uint16_t* residual;   // f16 [m, n]
+  uint16_t* y;                // f16 [m, n]
+  uint32_t m, n, k;
+  int act;                    // kaio_activation
+};
+// workgroups of a call
+constexpr uint64_t linear_wgs(uint64_t m, uint64_t n) { return (m + 15) / 16 * ((n + 15) / 16); }
+hipError_t launch_linear_w4a16(const LinearProblem& p, hipStream_t stream);
+
+constexpr uint32_t kMaxAxes = 8;
+struct RopeAppend {
+  PagedKV kv;
+  const uint16_t *q, *k_new, *v_new;   // [tokens, heads, head_dim]
+  uint16_t* q_out;
+  const int32_t* positions;            // [axes, tokens]
+  const double* inv_freq;              // [half]
+  uint32_t first_pair[kMaxAxes];       // first pair of each axis
+  uint32_t axes, half, q_heads;
+  FastDiv per_head;                    // items per head of the vector form (head_dim / 16)
+  bool bf16, interleaved;
+};
+hipError_t launch_rope_append(const RopeAppend& p, hipStream_t stream);
+
+struct PagedAttention {
+  PagedKV kv;
+  const uint16_t* q;                   // [tokens, q_heads, head_dim]
+  uint16_t* out;
+  void* workspace;
+  uint32_t q_heads, max_new;
+  FastDiv group;                       // q heads per K/V head
+  float scale;
+  uint32_t window, sinks;              // window 0: none
+  bool bf16;
+};
+constexpr uint64_t paged_attention_workspace(uint32_t, uint32_t, uint32_t, uint32_t, uint32_t, uint32_t) { return 0; }
+hipError_t launch_paged_attention(const PagedAttention& p, hipStream_t stream);
+
 hipError_t launch_dequant_group_bwd(kaio_dtype dtype, int64_t outer, int64_t axis,
                                     int64_t group, const void* dy, const void* scale,
                                     void* dq, hipStream_t stream);

@@ -1,0 +1,226 @@
+"""Attention over the paged cache on the GPU against the float64 oracle (tolerance: oracle.paged.attention_tolerance)."""
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_w4a16_amd as kaio
+from tests.gpu_util import DEV
+from tests.paged_util import Batch, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 128), (8, 2, 128), (6, 2, 64), (8, 1, 64), (14, 2, 128), (40, 2, 128)])
+def test_decode(dtype, hq, hkv, d):
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 127, 128, 129, 300]
+    b = Batch([1] * len(lens), lens, hq, hkv, d, 16, dtype, seed=d + hq)
+    b.check(b.attention())
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 64, 128, 512])
+def test_page_sizes(page):
+    b = Batch([1, 1, 1], [700, 65, 3], 4, 2, 128, page, "f16", seed=page)
+    b.check(b.attention())
+    b = Batch([70, 1, 33], [140, 65, 33], 4, 2, 64, page, "bf16", seed=page + 1)
+    b.check(b.attention())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 128), (4, 1, 64), (6, 2, 128), (7, 1, 64)])
+@pytest.mark.parametrize("new,lens", [([130], [130]), ([1, 64, 17], [200, 64, 81]), ([65, 2], [65, 259]),
+                                      ([129, 31, 0, 1], [129, 420, 9, 1])])
+def test_chunks(dtype, hq, hkv, d, new, lens):
+    b = Batch(new, lens, hq, hkv, d, 16, dtype, seed=sum(new) + hq)
+    b.check(b.attention())
+
+
+def test_long_axis_few_rows():
+    # one row over a long axis, and a few rows: the keys of a row are split over workgroups and joined
+    for new, hq, hkv in ((1, 2, 1), (3, 4, 2)):
+        b = Batch([new], [5003], hq, hkv, 128, 64, "f16", seed=new)
+        b.check(b.attention())
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 60, 150)]
+    new = [min(1, x) for x in lens]
+    b = Batch(new, lens, 2, 1, 64, 8, "f16", seed=3)
+    b.check(b.attention())
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (33, 4), (64, 70), (100, 1), (400, 4), (7, 1000)])
+@pytest.mark.parametrize("new,lens", [([1, 1, 1, 1], [1, 64, 301, 450]), ([40, 3, 129], [300, 450, 129])])
+def test_window_and_sinks(window, sinks, new, lens):
+    for d, page in ((64, 16), (128, 8)):
+        b = Batch(new, lens, 4, 2, d, page, "f16", seed=window + sinks, window=window, sinks=sinks)
+        b.check(b.attention())
+
+
+@pytest.mark.parametrize("d", [8, 40, 80, 96, 256])
+def test_other_head_dims(d):
+    b = Batch([1, 5], [70, 133], 4, 2, d, 16, "f16", seed=d)
+    b.check(b.attention())
+
+
+def test_rows_that_see_nothing_and_padding():
+    # a sequence whose every page is gone, one with new tokens but length 0, rows past the last sequence
+    for new in ([1, 1, 1], [40, 30, 50]):
+        b = Batch(new, [60, 70, 50], 4, 2, 64, 16, "f16", seed=9, pad=5)
+        b.table[1] = -1
+        b.lens[2] = 0
+        out = b.attention()
+        b.check(out)
+        y = f64(out)
+        assert not y[new[0]:].any()
+
+
+def test_pages_gone_in_the_middle_and_bad_ids():
+    for new in ([1], [50]):
+        b = Batch(new, [333], 4, 2, 128, 16, "bf16", seed=2)
+        b.table[0, 3] = -1
+        b.table[0, 7] = b.pages          # one past the last page: not there
+        b.table[0, 8] = -2 ** 31
+        b.check(b.attention())
+
+
+@pytest.mark.parametrize("new", [1, 3, 90])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_what_invisible_slots_hold_does_not_matter(new, bad):
+    # slots past the length, released pages and slots of no sequence hold NaN or infinities
+    b = Batch([new, new], [203, 90], 4, 2, 64, 16, "f16", seed=4, window=50, sinks=3)
+    ref = b.attention()
+    b.check(ref)
+    hide = ~b.used()
+    for c in (b.k_cache, b.v_cache):
+        c.view(-1, *c.shape[2:])[hide] = bad
+    out = b.attention()
+    assert torch.equal(ref, out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_masked_token_does_not_reach_the_rows_before_it(d, bad):
+    # token 37's K and V are not finite: rows before it are as without it, and rows past its window too
+    b = Batch([100], [100], 4, 2, d, 16, "f16", seed=6, window=20, sinks=2)
+    ref = f64(b.attention())
+    for c in (b.k_cache, b.v_cache):
+        c[b.table[0, 37 // 16], 37 % 16] = bad
+    out = f64(b.attention())
+    ok = [t for t in range(100) if t < 37 or t >= 57]
+    assert np.array_equal(out[ok], ref[ok])
+    assert not np.isfinite(out[37:57]).any()
+
+
+def test_visible_infinities_follow_the_formula():
+    b = Batch([1], [40], 1, 1, 64, 16, "f16", seed=8)
+    b.v_cache[b.table[0, 1], 2, 0, 5] = float("inf")
+    b.v_cache[b.table[0, 0], 3, 0, 6] = float("nan")
+    out = f64(b.attention())[0, 0]
+    assert out[5] == np.inf and np.isnan(out[6]) and np.isfinite(np.delete(out, [5, 6])).all()
+    # scores of minus infinity weigh nothing
+    b = Batch([1], [40], 1, 1, 64, 16, "f16", seed=8)
+    b.q[0, 0, 0] = 1.0
+    b.k_cache[b.table[0, 2], 1, 0, 0] = -float("inf")
+    b.check(b.attention())
+
+
+def test_lowest_values():
+    # the type's lowest value in K: scores far below the others, weights zero, nothing overflows to NaN
+    b = Batch([1, 40], [50, 77], 2, 1, 64, 16, "f16", seed=12)
+    b.q[:, :, 0] = 1.0
+    b.k_cache[b.table[0, 1], 3, 0, 0] = -65504.0
+    b.k_cache[b.table[1, 1], 3, 0, 0] = -65504.0
+    b.check(b.attention())
+
+
+def test_growing_scores():
+    # scores that rise along the axis: the running maximum moves at every block
+    b = Batch([1, 64], [900, 700], 2, 1, 64, 16, "f16", seed=13)
+    b.q.fill_(1.0)
+    for s in range(2):
+        for c in range(b.lens[s]):
+            b.k_cache[b.table[s, c // 16], c % 16] = c / 16.0
+    b.scale = 1.0 / 8
+    b.check(b.attention())
+
+
+def test_max_new_is_only_a_hint():
+    b = Batch([1, 40, 3], [60, 70, 200], 4, 2, 128, 16, "f16", seed=14)
+    b.check(b.attention())
+    for hint in (1, 2, 1000):
+        out = torch.full_like(b.dq, float("nan"))
+        kaio.kaio_paged_attention(b.dq, b.paged, hint, b.scale, out=out)
+        torch.cuda.synchronize()
+        b.check(out)
+
+
+def test_empty_batches():
+    b = Batch([], [], 4, 2, 64, 16, "f16", pad=3)
+    out = b.attention()
+    assert not out.any()
+    assert kaio.kaio_paged_attention(b.dq[:0], b.paged, 1, 1.0).shape == (0, 4, 64)
+
+
+def test_repeats_are_bit_equal_and_inputs_untouched():
+    b = Batch([1, 1, 1, 90], [900, 31, 77, 400], 8, 2, 128, 16, "bf16", seed=15)
+    a = b.attention()
+    keep = [t.clone() for t in (b.dq, b.dk, b.dv)]
+    for _ in range(3):
+        out = torch.empty_like(a)
+        kaio.kaio_paged_attention(b.dq, b.paged, 90, b.scale, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(a, out)
+    assert all(torch.equal(x, y) for x, y in zip(keep, (b.dq, b.dk, b.dv)))
+
+
+def test_side_stream_and_graph_replays():
+    b = Batch([1] * 5, [400, 31, 77, 1, 900], 8, 2, 128, 16, "f16", seed=16)
+    ref = b.attention()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = kaio.kaio_paged_attention(b.dq, b.paged, 1, b.scale)
+    side.synchronize()
+    assert torch.equal(ref, out)
+    out = kaio.kaio_paged_attention(b.dq, b.paged, 1, b.scale, stream=side)   # allocated here, used there
+    side.synchronize()
+    assert torch.equal(ref, out)
+    need = kaio.lib().kaio_paged_attention_workspace_size(b.paged._ref, 5, 8, 1)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        kaio.kaio_paged_attention(b.dq, b.paged, 1, b.scale, out=out, workspace=ws)
+    for i in range(3):          # lengths change between replays, in place
+        b.lens = [400 - i, 31 + i, 60, 1, 900 - 100 * i]
+        b.paged.lens.copy_(torch.tensor(b.lens, dtype=torch.int32))
+        b.dq.normal_(generator=torch.Generator(device=DEV).manual_seed(i))
+        b.q = b.dq.cpu()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        b.check(out)
+        eager = kaio.kaio_paged_attention(b.dq, b.paged, 1, b.scale)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, out)
+
+
+def test_large_offsets():
+    # a cache of more than 2^32 bytes: the sequence's pages at its far end
+    page, hkv, d = 64, 8, 128
+    pages = (2 ** 32 // (page * hkv * d * 2)) + 40
+    small = Batch([1], [200], 8, hkv, d, page, "f16", seed=17)
+    ref = small.attention()
+    k = torch.empty((pages, page, hkv, d), dtype=torch.float16, device=DEV)
+    v = torch.empty_like(k)
+    far = pages - small.pages
+    k[far:].copy_(small.dk)
+    v[far:].copy_(small.dv)
+    table = torch.where(small.table >= 0, small.table + far, small.table)
+    paged = kaio.KaioPagedKV(k, v, table.to(DEV), small.q_start.to(DEV), torch.tensor([200], dtype=torch.int32, device=DEV))
+    out = kaio.kaio_paged_attention(small.dq, paged, 1, small.scale)
+    torch.cuda.synchronize()
+    assert torch.equal(ref, out)
+    del k, v
