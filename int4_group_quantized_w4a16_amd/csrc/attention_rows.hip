@@ -1,4 +1,5 @@
-// Attention of new tokens over the paged cache -- one wave per row and head.
+// Attention over the paged cache, by rows: one wave per row and head, for head
+// sizes that the matrix-instruction forms do not have.
 //
 //   o = sum_c p_c v_c / sum_c p_c,  p_c = exp(scale * q.k_c - m),  m = max
 //
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(64) paged_attention_rows_kernel(PagedAttention
 
 }  // namespace
 
-hipError_t launch_paged_attention(const PagedAttention& p, hipStream_t stream) {
+hipError_t launch_attention_rows(const PagedAttention& p, hipStream_t stream) {
   const dim3 grid(p.kv.tokens * p.q_heads);
   if (p.bf16)
     hipLaunchKernelGGL((paged_attention_rows_kernel<true>), grid, dim3(64), 0, stream, p);

@@ -1,0 +1,219 @@
+// Work of one paged-attention call: tiles of packed rows, blocks of keys, and
+// which workgroup takes which.
+//
+// Packed rows.  The g = q_heads / kv_heads query heads that share a K/V head
+// read the same keys, so the rows of a (sequence, K/V head) are numbered
+// token * g + head and cut into tiles of R rows: one pass over the keys serves
+// every head of the group.
+//
+// Blocks.  A tile sees the keys of `count` blocks of B: all from 0 up to its
+// last row's position, or with a window the ns blocks that hold the sinks and
+// those from the first row's window on; blocks between them are never touched.
+// A tile that sees nothing still counts as one unit, in which its zeros are
+// written.
+//
+// Split form.  The units of all tiles, K/V head by K/V head, form one line
+// that is cut into equal parts, one per workgroup, wherever the cuts fall:
+// lengths may differ as they like.  A tile inside one part is finished there;
+// a part's first piece (of a tile begun earlier) and its last (of a tile that
+// goes on) are partial results -- running maximum, sum and unnormalized
+// output in f32 -- in the workspace, slots 2w and 2w + 1 of workgroup w, and a
+// second kernel joins each tile's pieces in order.  The lengths are only known
+// on the device, so every workgroup derives the line from them by itself.
+//
+// Direct form, for calls with so many tiles that they balance by themselves:
+// one workgroup per tile and K/V head, nothing to join.
+#pragma once
+
+#include "launch.hpp"
+#include "paged.hpp"
+
+namespace kaio {
+
+struct Tile {
+  uint32_t seq;
+  uint32_t row0, rows;      // packed rows of the sequence
+  int32_t q0;               // row of q of the sequence's first new token
+  int32_t p0, p1;           // positions of the tile's first and last row
+  int32_t hi;               // keys from here on are not visible to any row
+  int32_t shift;            // position of row t of q = t + shift
+  uint32_t ns, wb0, count;  // blocks: ns from 0, then from wb0
+};
+
+__device__ __forceinline__ int32_t clamp_row(int32_t x, uint32_t tokens) {
+  return x < 0 ? 0 : x > (int32_t)tokens ? (int32_t)tokens : x;
+}
+// rows of q of sequence s (all of them inside q whatever q_start holds)
+__device__ __forceinline__ void seq_rows(const PagedKV& kv, uint32_t s, int32_t& a, int32_t& b) {
+  a = clamp_row(kv.q_start[s], kv.tokens);
+  b = clamp_row(kv.q_start[s + 1], kv.tokens);
+  if (b < a) b = a;
+}
+template <uint32_t R>
+__device__ __forceinline__ uint32_t seq_tiles(const PagedAttention& p, uint32_t s) {
+  int32_t a, b;
+  seq_rows(p.kv, s, a, b);
+  return ((uint32_t)(b - a) * p.group.d + R - 1) / R;
+}
+
+template <uint32_t R, uint32_t B>
+__device__ __forceinline__ Tile tile_info(const PagedAttention& p, uint32_t s, uint32_t i) {
+  Tile t;
+  int32_t a, b;
+  seq_rows(p.kv, s, a, b);
+  const uint32_t g = p.group.d, rows = (uint32_t)(b - a) * g;
+  const int32_t len = p.kv.lens[s] > 0 ? p.kv.lens[s] : 0;
+  t.seq = s;
+  t.q0 = a;
+  t.row0 = i * R;
+  t.rows = rows - t.row0 < R ? rows - t.row0 : R;
+  t.shift = len - p.kv.q_start[s + 1];
+  t.p0 = a + (int32_t)p.group.div(t.row0) + t.shift;
+  t.p1 = a + (int32_t)p.group.div(t.row0 + t.rows - 1) + t.shift;
+  t.hi = t.p1 < (int32_t)p.kv.cap ? t.p1 + 1 : (int32_t)p.kv.cap;
+  t.ns = t.wb0 = t.count = 0;
+  if (t.hi <= 0) {
+    t.hi = 0;
+    return t;
+  }
+  const uint32_t nb = ((uint32_t)t.hi + B - 1) / B;
+  if (p.window == 0) {
+    t.count = nb;
+    return t;
+  }
+  const int64_t lo = (int64_t)t.p0 - p.window + 1;
+  const uint32_t sinks = p.sinks < (uint32_t)t.hi ? p.sinks : (uint32_t)t.hi;
+  t.ns = (sinks + B - 1) / B;
+  const uint32_t w = lo > 0 ? (uint32_t)lo / B : 0;
+  t.wb0 = w > t.ns ? w : t.ns;
+  t.count = t.ns + (nb > t.wb0 ? nb - t.wb0 : 0);
+  return t;
+}
+__device__ __forceinline__ uint32_t units_of(const Tile& t) { return t.count ? t.count : 1; }
+
+// Positions a row does not see below: a row at pos sees c > this or c < sinks.
+__device__ __forceinline__ int32_t window_floor(const PagedAttention& p, int32_t pos) {
+  if (p.window == 0) return -1;
+  const int64_t f = (int64_t)pos - p.window;
+  return f < -1 ? -1 : (int32_t)f;
+}
+
+// ---- the direct form: tile `index` of one K/V head; false past the last ----
+template <uint32_t R>
+__device__ __forceinline__ bool direct_tile(const PagedAttention& p, uint32_t index, uint32_t lane, uint32_t& seq,
+                                            uint32_t& i) {
+  uint32_t base = 0;
+  for (uint32_t s0 = 0; s0 < p.kv.seqs; s0 += 64) {
+    const uint32_t s = s0 + lane;
+    uint32_t n = s < p.kv.seqs ? seq_tiles<R>(p, s) : 0, end = n;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const uint32_t o = __shfl_up(end, x);
+      end += lane >= (uint32_t)x ? o : 0;
+    }
+    const uint64_t past = __ballot(base + end > index);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      seq = s0 + l;
+      i = index - (base + __builtin_amdgcn_readlane(end, l) - __builtin_amdgcn_readlane(n, l));
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(end, 63);
+  }
+  return false;
+}
+
+// ---- the split form ---------------------------------------------------------
+constexpr uint32_t kSchedThreads = 256;
+constexpr uint32_t kSchedPer = kSchedTiles / kSchedThreads;
+
+struct Line {
+  uint32_t first[kSchedTiles + 1];   // first tile of each sequence
+  uint32_t start[kSchedTiles + 1];   // first unit of each tile
+  uint32_t wave_sum[kSchedThreads / 64];
+};
+
+// exclusive prefix sums of v[kSchedPer] per thread (thread order), written to dst[0 .. n], the total in dst[n]
+__device__ __forceinline__ void block_scan(const uint32_t (&v)[kSchedPer], uint32_t n, uint32_t* dst, uint32_t* wave_sum) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t sum = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kSchedPer; ++k) sum += v[k];
+  uint32_t end = sum;
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const uint32_t o = __shfl_up(end, x);
+    end += lane >= (uint32_t)x ? o : 0;
+  }
+  if (lane == 63) wave_sum[wave] = end;
+  __syncthreads();
+  uint32_t at = end - sum;
+#pragma unroll
+  for (uint32_t w = 0; w < kSchedThreads / 64; ++w) at += w < wave ? wave_sum[w] : 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kSchedPer; ++k) {
+    if (tid * kSchedPer + k <= n) dst[tid * kSchedPer + k] = at;
+    at += v[k];
+  }
+  if (tid == kSchedThreads - 1 && n == kSchedTiles) dst[n] = at;
+  __syncthreads();
+}
+
+// index of the part of [0, n) that holds x: the last i with start[i] <= x (start[0] = 0, start[n] > x)
+__device__ __forceinline__ uint32_t part_of(const uint32_t* start, uint32_t n, uint32_t x) {
+  uint32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Builds the line (every thread of a kSchedThreads workgroup); returns the tile count.
+// seqs <= kSchedTiles and the host's bound on the tiles <= kSchedTiles hold in the split form.
+template <uint32_t R, uint32_t B>
+__device__ __forceinline__ uint32_t build_line(const PagedAttention& p, Line& line) {
+  const uint32_t tid = threadIdx.x, n = p.kv.seqs;
+  uint32_t v[kSchedPer];
+#pragma unroll
+  for (uint32_t k = 0; k < kSchedPer; ++k) {
+    const uint32_t s = tid * kSchedPer + k;
+    v[k] = s < n ? seq_tiles<R>(p, s) : 0;
+  }
+  block_scan(v, n, line.first, line.wave_sum);
+  // overlapping sequences (q_start not ascending) could have more tiles than rows: those past the bound are dropped
+  const uint32_t tiles = line.first[n] < kSchedTiles ? line.first[n] : kSchedTiles;
+#pragma unroll
+  for (uint32_t k = 0; k < kSchedPer; ++k) {
+    const uint32_t i = tid * kSchedPer + k;
+    v[k] = 0;
+    if (i < tiles) {
+      const uint32_t s = part_of(line.first, n, i);
+      v[k] = units_of(tile_info<R, B>(p, s, i - line.first[s]));
+    }
+  }
+  block_scan(v, tiles, line.start, line.wave_sum);
+  return tiles;
+}
+
+// The cut of `total` units over `parts` workgroups.
+struct Cut {
+  uint32_t per, rem;
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * per + (w < rem ? w : rem); }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+    const uint32_t big = rem * (per + 1);
+    return u < big ? u / (per + 1) : rem + (u - big) / per;
+  }
+};
+// no part shorter than kMinUnits where there are fewer units than that for everyone
+template <uint32_t kMinUnits>
+__device__ __forceinline__ Cut cut_of(uint32_t total, uint32_t workers) {
+  uint32_t parts = (total + kMinUnits - 1) / kMinUnits;
+  parts = parts < workers ? parts : workers;
+  parts = parts ? parts : 1;
+  const uint32_t per = total / parts;
+  return Cut{per, total - per * parts};
+}
+
+}  // namespace kaio

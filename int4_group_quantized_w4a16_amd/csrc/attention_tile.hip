@@ -1,0 +1,365 @@
+// Attention over the paged cache, tile form: many rows (prompts, chunks).
+//
+// gfx950 design
+// -------------
+// * Workgroup = 4 waves, 128 packed rows (token * group + head) of one
+//   (sequence, K/V head); wave w owns rows 32w .. 32w+31 and keeps their Q
+//   fragments, running maximum, sum and output in registers.  Keys pass in
+//   blocks of 64 through two LDS buffers shared by the waves (33 KiB each at
+//   128 columns), so two workgroups share a CU and one's softmax runs under
+//   the other's matrix instructions.
+// * Scores are computed transposed, S^T = K.Q^T (32x32x16 MFMA, K the A
+//   operand): a lane then holds, for ITS row, 16 keys of each 32, and their
+//   weights in exactly the order in which it feeds them to the second product
+//   O^T = V^T.P^T as B operand, with k index (h, j) standing for key
+//   8 (j / 4) + 4 h + j % 4 of 16.  Weights never leave the lane; V^T comes
+//   from transposed LDS reads of four keys each in the same order.
+// * K rows are padded by 16 bytes (the 16 lanes of a 16-byte read step
+//   through all banks), V rows are swizzled (64-byte windows xor row % 4) for
+//   the transposed reads.
+// * The block's cache rows are fetched one block ahead into registers, by
+//   slot: lane j of each wave looks up the slot of key j (another block
+//   ahead), rows are shared by permutes, so pages of any size work and every
+//   address is 64 bits.
+// * Softmax in f32 with base-2 exponents: p = 2^(c s - m), c = scale * log2 e
+//   folded into one FMA; m lags (kLag).  Weights are rounded to the 16-bit
+//   type for the second product, the sum is taken of the unrounded ones.
+// * Masks are applied only in blocks that some row does not wholly see, by
+//   selects on scores; V of slots that are not there is zeroed on the way to
+//   LDS, and non-finite V of a token that some rows see and others do not is
+//   kept away from the latter (see `special`).
+
+#include "attention_common.hpp"
+
+namespace kaio {
+namespace {
+
+constexpr uint32_t R = kTileRows, B = kTileKeys;
+static_assert(R == 128 && B == 64, "four waves of 32 rows, blocks of two 32-key score tiles");
+
+template <int D>
+struct Lds {
+  static constexpr int kKRow = D * 2 + 16;   // bytes of a padded K row
+  static constexpr int kVRow = D * 2;
+  static constexpr int kV = B * kKRow;       // offset of V in a buffer
+  static constexpr int kSize = kV + B * kVRow;
+};
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p, bool split, uint32_t tiles_bound) {
+  using L = Lds<D>;
+  constexpr int KS = D / 16;            // k steps of the first product
+  constexpr int DT = D / 32;            // 32-column tiles of the output
+  constexpr int CPR = D / 8;            // 16-byte chunks per row
+  constexpr int RPL = 256 / CPR;        // rows per pass of the 256 threads' loads
+  constexpr int NL = B / RPL;           // passes
+  __shared__ __attribute__((aligned(256))) char buf[2][L::kSize];
+  __shared__ uint32_t flags[2][4];      // per buffer and wave: V holds non-finite values
+  extern __shared__ char dyn[];
+  Line& line = *reinterpret_cast<Line*>(dyn);   // split form only
+
+  const PagedKV& kv = p.kv;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t g = p.group.d;
+  const size_t row_elems = (size_t)kv.kv_heads * D;       // a cache slot
+  const bool negate = p.scale < 0.f;
+  const float c = fmaxf(fabsf(p.scale) * 1.44269504088896341f, 1.17549435e-38f);
+
+  zero_unowned(p, blockIdx.x, gridDim.x);
+
+  // what this workgroup does: one whole tile, or a part of the line
+  uint32_t unit = 0, end = 1, total = 0, tiles = 0, head = 0, seq = 0, tile_in_seq = 0, tile = 0;
+  const uint32_t wg = xcd_remap(blockIdx.x, gridDim.x);
+  if (split) {
+    tiles = build_line<R, B>(p, line);
+    total = line.start[tiles];
+    if (tiles == 0) return;
+    const Cut cut = cut_of<kTileMinUnits>(total * kv.kv_heads, gridDim.x);
+    unit = cut.start(wg);
+    end = cut.start(wg + 1);
+    if (end > total * kv.kv_heads) end = total * kv.kv_heads;
+    if (unit >= end) return;
+    head = unit / total;
+    tile = part_of(line.start, tiles, unit - head * total);
+  } else {
+    head = wg / tiles_bound;
+    // later tiles see more keys: they start first
+    if (!direct_tile<R>(p, tiles_bound - 1 - wg % tiles_bound, lane, seq, tile_in_seq)) return;
+  }
+
+  bool first_piece = true;
+  while (unit < end) {
+    uint32_t b0 = 0;
+    if (split) {
+      if (tile == tiles) {
+        tile = 0;
+        ++head;
+      }
+      seq = part_of(line.first, kv.seqs, tile);
+      tile_in_seq = tile - line.first[seq];
+      b0 = unit - head * total - line.start[tile];
+    }
+    const Tile t = tile_info<R, B>(p, seq, tile_in_seq);
+    uint32_t b1 = units_of(t);
+    const uint32_t whole = b1;
+    if (split && b1 - b0 > end - unit) b1 = b0 + (end - unit);
+    const bool complete = b0 == 0 && b1 == whole;
+    if (!first_piece) __syncthreads();   // the previous piece's last block is no longer read
+
+    // ---- this lane's row ----
+    const uint32_t r = wave * 32 + l32 < t.rows ? wave * 32 + l32 : t.rows - 1;
+    const uint32_t pr = t.row0 + r, tok = p.group.div(pr);
+    const size_t qrow = ((size_t)(t.q0 + (int32_t)tok) * p.q_heads + head * g + (pr - tok * g)) * D;
+    const int32_t pos = t.q0 + (int32_t)tok + t.shift;
+    const int32_t floor = window_floor(p, pos);
+    const int32_t sinks = p.window ? (int32_t)(p.sinks < 0x7FFFFFFFu ? p.sinks : 0x7FFFFFFFu) : 0;
+    // rows are in order of their positions: the wave's first and last
+    const int32_t wpos0 = __builtin_amdgcn_readlane(pos, 0), wpos1 = __builtin_amdgcn_readlane(pos, 31);
+    const int32_t wfloor1 = __builtin_amdgcn_readlane(floor, 31);
+    const int32_t tfloor1 = window_floor(p, t.p1);
+
+    short8_t q[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q[k] = *reinterpret_cast<const short8_t*>(p.q + qrow + k * 16 + h * 8);
+      if (negate) q[k] ^= (short)0x8000;
+    }
+    floatx16 o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    const uint32_t nblk = t.count ? b1 - b0 : 0;    // a tile that sees nothing has no blocks
+    auto key0_of = [&](uint32_t i) {                // first key of the piece's block i
+      const uint32_t b = b0 + i;
+      return (int32_t)((b < t.ns ? b : t.wb0 + (b - t.ns)) * B);
+    };
+    // slot of key `lane` of block i
+    auto slots = [&](uint32_t i) {
+      const int32_t k = key0_of(i) + (int32_t)lane;
+      return i < nblk && k < t.hi ? slot_of(kv, t.seq, k) : -1;
+    };
+    u32x4 kr[NL], vr[NL];
+    const uint32_t lrow = tid / CPR, lch = tid % CPR;   // this thread's row and chunk of a pass
+    auto fetch = [&](int32_t slot) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int32_t s = __shfl(slot, (int)(i * RPL + lrow));
+        const size_t at = (size_t)(s < 0 ? 0 : s) * row_elems + head * D + lch * 8;
+        kr[i] = *reinterpret_cast<const u32x4*>(kv.k + at);
+        vr[i] = *reinterpret_cast<const u32x4*>(kv.v + at);
+      }
+    };
+    // the block's rows to LDS; V of absent slots as zeros
+    auto store = [&](uint32_t buffer, int32_t slot, uint64_t live, bool edge) {
+      if (~live) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          if (__shfl(slot, (int)(i * RPL + lrow)) < 0) vr[i] = u32x4{0, 0, 0, 0};
+      }
+      if (edge) {
+        bool special = false;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) special |= any_special<kBf16>(vr[i][e]);
+        flags[buffer][wave] = __ballot(special) != 0;
+      }
+      char* const b = buf[buffer];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t row = i * RPL + lrow;
+        *reinterpret_cast<u32x4*>(b + row * L::kKRow + lch * 16) = kr[i];
+        const uint32_t swz = D == 128 ? (row & 3) : ((row >> 1) & 1);
+        *reinterpret_cast<u32x4*>(b + L::kV + row * L::kVRow + ((lch * 16) ^ (swz * 64))) = vr[i];
+      }
+    };
+    // some row of the tile does not see some key of the block that starts at key0
+    auto edge_of = [&](int32_t key0) {
+      return key0 + (int32_t)B - 1 > t.p0 || (p.window && key0 <= tfloor1 && key0 + (int32_t)B > sinks);
+    };
+
+    int32_t slot = slots(0), slot_next = slots(1);
+    uint64_t live = __ballot(slot >= 0);
+    if (nblk) {
+      if (live) fetch(slot);
+      store(0, slot, live, edge_of(key0_of(0)));
+    }
+    __syncthreads();
+
+    for (uint32_t i = 0; i < nblk; ++i) {
+      const int32_t key0 = key0_of(i);
+      const char* const kb = buf[i & 1];
+      const char* const vb = kb + L::kV;
+      const uint64_t live_next = __ballot(slot_next >= 0);
+      if (live_next) fetch(slot_next);
+      const int32_t slot_after = slots(i + 2);
+
+      // does any of the wave's rows see any of the block's keys?
+      if (live && key0 <= wpos1) {
+        floatx16 s[2];
+        const char* const kl = kb + l32 * L::kKRow + h * 16;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[st][e] = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            s[st] = mfma32<kBf16>(*reinterpret_cast<const short8_t*>(kl + st * 32 * L::kKRow + k * 32), q[k], s[st]);
+        }
+        // element e of tile st is key 32 st + 8 (e / 4) + 4 h + e % 4
+        const bool edge = key0 + (int32_t)B - 1 > wpos0 || (p.window && key0 <= wfloor1 && key0 + (int32_t)B > sinks);
+        if (edge || ~live) {
+          const uint32_t lo32 = (uint32_t)(live >> (4 * h)), hi32 = (uint32_t)(live >> (32 + 4 * h));
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int off = 8 * (e / 4) + e % 4;
+              const int32_t key = key0 + 32 * st + off + 4 * (int32_t)h;
+              const bool sees = key <= pos && (key > floor || key < sinks) && (((st ? hi32 : lo32) >> off) & 1);
+              s[st][e] = sees ? s[st][e] : -INFINITY;
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+        top = max_halves(top) * c;
+        if (__any(top > m + kLag)) {
+          const float m1 = fmaxf(m, top);
+          const float old = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
+          l *= old;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] *= old;
+          m = m1;
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        short8_t w[4];     // weights: k step 2 st + (e >= 8), elements e % 8
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            u32x4 pk;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float a = exp2_fast(__builtin_fmaf(s[st][8 * e2 + e], c, base));
+              const float b = exp2_fast(__builtin_fmaf(s[st][8 * e2 + e + 1], c, base));
+              l += a;
+              l += b;
+              pk[e / 2] = pack2<kBf16>(a, b);
+            }
+            w[2 * st + e2] = __builtin_bit_cast(short8_t, pk);
+          }
+        // V^T fragment of k step ks, columns 32 d ..: keys 16 ks + 4 h + (0..3), and 8 further on
+        const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
+        const uint32_t vswz = (D == 128 ? (vrow & 3) : ((vrow >> 1) & 1)) * 64;
+        const uint32_t vcol = (lane & 16) * 2 + (lane & 3) * 8;
+        auto vfrag = [&](int ks, int d) {
+          const char* const a = vb + vrow * L::kVRow + ks * 16 * L::kVRow + ((d * 64 + vcol) ^ vswz);
+          return join(read_tr(a), read_tr(a + 8 * L::kVRow));
+        };
+        const bool special = edge_of(key0) && (flags[i & 1][0] | flags[i & 1][1] | flags[i & 1][2] | flags[i & 1][3]);
+        if (!special) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vfrag(ks, d), w[ks], o[d]);
+        } else {
+          // Weight 0 times a non-finite V is not 0: the finite values go through the product, the others are counted
+          // per row over the keys it sees, and put in where the count is not zero.
+          constexpr short one = kBf16 ? 0x3F80 : 0x3C00;
+          short8_t sees[4];
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sees[ks][e] = s[ks >> 1][8 * (ks & 1) + e] == -INFINITY ? (short)0 : one;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            floatx16 nan, inf, neg;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) nan[e] = inf[e] = neg[e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const Special<kBf16> v(vfrag(ks, d));
+              o[d] = mfma32<kBf16>(v.fin, w[ks], o[d]);
+              nan = mfma32<kBf16>(v.nan, sees[ks], nan);
+              inf = mfma32<kBf16>(v.pos, sees[ks], inf);
+              neg = mfma32<kBf16>(v.neg, sees[ks], neg);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] = with_special(o[d][e], nan[e], inf[e], neg[e]);
+          }
+        }
+      }
+      if (i + 1 < nblk) store((i + 1) & 1, slot_next, live_next, edge_of(key0_of(i + 1)));
+      slot_next = slot_after;
+      live = live_next;
+      __syncthreads();
+    }
+
+    // ---- the piece's result ----
+    l = add_halves(l);
+    const bool mine = wave * 32 + l32 < t.rows;
+    if (complete) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          // columns 32 d + 8 j + 4 h + (0..3) and 8 further on; exchanging halves gives each lane 8 in a row
+          uint32_t a0 = pack2<kBf16>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv);
+          uint32_t a1 = pack2<kBf16>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv);
+          uint32_t c0 = pack2<kBf16>(o[d][4 * j + 4] * inv, o[d][4 * j + 5] * inv);
+          uint32_t c1 = pack2<kBf16>(o[d][4 * j + 6] * inv, o[d][4 * j + 7] * inv);
+          const auto x0 = __builtin_amdgcn_permlane32_swap(a0, c0, false, false);
+          const auto x1 = __builtin_amdgcn_permlane32_swap(a1, c1, false, false);
+          if (mine)
+            *reinterpret_cast<u32x4*>(p.out + qrow + 32 * d + 8 * (j + (int)h)) =
+                u32x4{(uint32_t)x0[0], (uint32_t)x1[0], (uint32_t)x0[1], (uint32_t)x1[1]};
+        }
+    } else {
+      float* const part = partial_of<R, D>(p, 2 * wg + (b0 == 0));
+      if (mine) {
+        float* const row = part + (size_t)r * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<floatx4*>(row + 32 * d + 8 * j) =
+                floatx4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+        if (h == 0) {
+          part[R * D + r] = m;
+          part[R * D + R + r] = l;
+        }
+      }
+    }
+    unit += split ? b1 - b0 : 1;
+    ++tile;
+    first_piece = false;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attention_tile(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream) {
+  const size_t lds = plan.split ? sizeof(Line) : 0;
+#define KAIO_TILE(BF, DIM)                                                                                   \
+  hipLaunchKernelGGL((attention_tile_kernel<BF, DIM>), dim3(plan.workgroups), dim3(256), lds, stream, p,     \
+                     plan.split, plan.tiles)
+  if (p.kv.head_dim == 128) {
+    if (p.bf16) KAIO_TILE(true, 128);
+    else KAIO_TILE(false, 128);
+  } else {
+    if (p.bf16) KAIO_TILE(true, 64);
+    else KAIO_TILE(false, 64);
+  }
+#undef KAIO_TILE
+  return hipGetLastError();
+}
+
+}  // namespace kaio

@@ -307,6 +307,11 @@ kaio::PagedKV paged_of(const kaio_paged_kv* kv, uint32_t tokens) {
   return p;
 }
 
+kaio::AttentionPlan attention_plan_of(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads, uint32_t max_new) {
+  return kaio::attention_plan(kv->kv_heads, q_heads, kv->head_dim, kv->seqs,
+                              (uint64_t)kv->table_width * kv->page_size, tokens, max_new);
+}
+
 }  // namespace
 
 extern "C" {
@@ -561,7 +566,7 @@ kaio_status kaio_rope_append(const kaio_paged_kv* kv, const void* q, const void*
 size_t kaio_paged_attention_workspace_size(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads,
                                            uint32_t max_new) {
   if (!kv || kv->kv_heads == 0 || q_heads % kv->kv_heads != 0 || kv->page_size == 0 || tokens == 0) return 0;
-  return kaio::paged_attention_workspace(kv->kv_heads, q_heads, kv->head_dim, kv->seqs, tokens, max_new);
+  return attention_plan_of(kv, tokens, q_heads, max_new).workspace;
 }
 
 kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* out, uint32_t tokens, uint32_t q_heads,
@@ -577,11 +582,13 @@ kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* o
   if (max_new == 0) return fail(KAIO_ERR_INVALID_PROBLEM, op, "max_new must be > 0");
   uint64_t cache_bytes = 0, table_bytes = 0, q_bytes = 0;
   if (!paged_fits(kv, &cache_bytes, &table_bytes) || (uint64_t)tokens * q_heads > kaio::kMaxWorkgroups ||
+      (uint64_t)kv->seqs * kv->kv_heads > kaio::kMaxWorkgroups / 2 ||
       !bytes_of(tokens, (uint64_t)q_heads * kv->head_dim, 2, &q_bytes))
-    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, q_heads=%u, slots=%llu)",
-                tokens, q_heads, (unsigned long long)kv->pages * kv->page_size);
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, q_heads=%u, seqs=%u, slots=%llu)",
+                tokens, q_heads, kv->seqs, (unsigned long long)kv->pages * kv->page_size);
   if (kaio_status st = check_paged_pointers(op, kv)) return st;
-  const uint64_t need = kaio::paged_attention_workspace(kv->kv_heads, q_heads, kv->head_dim, kv->seqs, tokens, max_new);
+  const kaio::AttentionPlan plan = attention_plan_of(kv, tokens, q_heads, max_new);
+  const uint64_t need = plan.workspace;
   if (!q) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input q is null");
   if (!out) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output out is null");
   if (need && !workspace) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace is null");
@@ -613,7 +620,11 @@ kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* o
   p.window = window;
   p.sinks = sinks;
   p.bf16 = kv->dtype == KAIO_DTYPE_BF16;
-  return launched(op, kaio::launch_paged_attention(p, static_cast<hipStream_t>(stream)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (plan.rows) return launched(op, kaio::launch_attention_rows(p, st));
+  const hipError_t e = plan.stream ? kaio::launch_attention_stream(p, plan, st) : kaio::launch_attention_tile(p, plan, st);
+  if (e != hipSuccess || !plan.split) return launched(op, e);
+  return launched(op, kaio::launch_attention_join(p, plan, st));
 }
 
 const char* kaio_last_error(void) { return g_last_error.c_str(); }

@@ -180,8 +180,38 @@ struct PagedAttention {
   uint32_t window, sinks;              // window 0: none
   bool bf16;
 };
-constexpr uint64_t paged_attention_workspace(uint32_t, uint32_t, uint32_t, uint32_t, uint32_t, uint32_t) { return 0; }
-hipError_t launch_paged_attention(const PagedAttention& p, hipStream_t stream);
+// How a call runs: head_dim 64 and 128 on matrix instructions, few rows per
+// sequence in the stream form, more in the tile form; other head_dims by rows.
+constexpr uint32_t kTileRows = 128, kTileKeys = 64, kTileMinUnits = 2;
+constexpr uint32_t kStreamRows = 16, kStreamKeys = 128, kStreamMinUnits = 1;
+constexpr uint32_t kSchedTiles = 1024;    // tiles (per K/V head) and sequences the split form's schedule holds
+struct AttentionPlan {
+  bool rows, stream, split;
+  uint32_t tiles;           // bound on the tiles of one K/V head
+  uint32_t workgroups;
+  uint64_t workspace;       // bytes
+};
+constexpr AttentionPlan attention_plan(uint32_t kv_heads, uint32_t q_heads, uint32_t head_dim, uint32_t seqs,
+                                       uint64_t cap, uint32_t tokens, uint32_t max_new) {
+  AttentionPlan a{};
+  a.rows = head_dim != 64 && head_dim != 128;
+  if (a.rows) return a;
+  const uint64_t g = q_heads / kv_heads;
+  a.stream = max_new * g <= kStreamRows;
+  const uint64_t rows = a.stream ? kStreamRows : kTileRows, keys = a.stream ? kStreamKeys : kTileKeys;
+  // every sequence's last tile may be short
+  const uint64_t tiles = tokens * g / rows + seqs;
+  a.tiles = tiles ? (uint32_t)tiles : 1;
+  const uint64_t slots = 2 * kComputeUnits;                 // workgroups resident at once
+  a.split = tiles <= kSchedTiles && a.tiles * kv_heads < 4 * slots && (cap / keys + 2) * a.tiles * kv_heads < (1ull << 31);
+  a.workgroups = (uint32_t)(a.split ? slots : a.tiles * kv_heads);
+  a.workspace = a.split ? slots * 2 * rows * (head_dim + 2) * 4 : 0;
+  return a;
+}
+hipError_t launch_attention_tile(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream);
+hipError_t launch_attention_stream(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream);
+hipError_t launch_attention_join(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream);
+hipError_t launch_attention_rows(const PagedAttention& p, hipStream_t stream);
 
 hipError_t launch_dequant_group_bwd(kaio_dtype dtype, int64_t outer, int64_t axis,
                                     int64_t group, const void* dy, const void* scale,

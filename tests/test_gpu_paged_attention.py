@@ -50,6 +50,24 @@ def test_many_sequences():
     b.check(b.attention())
 
 
+def test_many_sequences_unsplit():
+    # so many tiles that each is one workgroup's: more sequences than the schedule holds, and many short chunks
+    rng = np.random.default_rng(6)
+    b = Batch([1] * 1100, [int(x) for x in rng.integers(1, 40, 1100)], 2, 1, 64, 8, "f16", seed=4)
+    b.check(b.attention())
+    b = Batch([5] * 140, [int(x) for x in rng.integers(5, 150, 140)], 64, 16, 64, 16, "bf16", seed=5, pad=3)
+    b.check(b.attention())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_negative_and_zero_scale(d):
+    for scale in (-0.1, 0.0):
+        for new in ([1, 1], [40, 3]):
+            b = Batch(new, [130, 77], 4, 2, d, 16, "f16", seed=11)
+            b.scale = scale
+            b.check(b.attention())
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (33, 4), (64, 70), (100, 1), (400, 4), (7, 1000)])
 @pytest.mark.parametrize("new,lens", [([1, 1, 1, 1], [1, 64, 301, 450]), ([40, 3, 129], [300, 450, 129])])
 def test_window_and_sinks(window, sinks, new, lens):
