@@ -78,6 +78,12 @@ __device__ __forceinline__ bool any_special(uint32_t w) {
   constexpr uint32_t e = kBf16 ? 0x7F807F80u : 0x7C007C00u, lsb = kBf16 ? 0x00800080u : 0x04000400u;
   return ((((w & e) + lsb) & 0x80008000u) != 0);   // the exponent field carries out only when full
 }
+// the same dword with its non-finite halves zeroed
+template <bool kBf16>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u;
+  return ((w & e) == e ? 0u : w & 0xFFFFu) | (((w >> 16) & e) == e ? 0u : w & 0xFFFF0000u);
+}
 template <bool kBf16>
 struct Special {   // split of eight values: the finite ones, and ones where NaN, +inf, -inf stand
   short8_t fin, nan, pos, neg;
@@ -98,6 +104,19 @@ __device__ __forceinline__ float with_special(float x, float nan, float pos, flo
   x += pos > 0.f ? INFINITY : 0.f;
   x -= neg > 0.f ? INFINITY : 0.f;
   return nan > 0.f ? NAN : x;
+}
+
+// Direct global -> LDS load of 16 bytes per lane: from base + off (base
+// wave-uniform) to lds + 16 * lane.  The buffer form, whose pending loads the
+// compiler does not hold against LDS reads; callers wait by wait_vm_barrier.
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+}
+// Waits until at most N vector-memory operations of the wave are outstanding, then meets the others.
+template <int N>
+__device__ __forceinline__ void wait_vm_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ short8_t join(short4_t a, short4_t b) {

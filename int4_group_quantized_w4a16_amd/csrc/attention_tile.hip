@@ -14,20 +14,27 @@
 //   O^T = V^T.P^T as B operand, with k index (h, j) standing for key
 //   8 (j / 4) + 4 h + j % 4 of 16.  Weights never leave the lane; V^T comes
 //   from transposed LDS reads of four keys each in the same order.
-// * K rows are padded by 16 bytes (the 16 lanes of a 16-byte read step
-//   through all banks), V rows are swizzled (64-byte windows xor row % 4) for
-//   the transposed reads.
-// * The block's cache rows are fetched one block ahead into registers, by
-//   slot: lane j of each wave looks up the slot of key j (another block
-//   ahead), rows are shared by permutes, so pages of any size work and every
-//   address is 64 bits.
+// * The cache rows of the next block go straight to LDS (direct loads) while
+//   the current one is computed on; one barrier per block.  Lane j of each
+//   wave looks up the slot of key j one block ahead of that.  A load covers 4
+//   (64 columns: 8) keys; where they share a page (page_size a multiple of
+//   that) it takes a wave-uniform 64-bit base and one lane offset, otherwise
+//   one load per key.
+// * LDS rows are unpadded (a direct load writes lane-contiguous chunks), so
+//   bank conflicts are avoided by where each 16-byte chunk is put: K chunk c
+//   of row r at c ^ (r % 16), V at its 64-byte window xor r % 4 (64 columns:
+//   the same over pairs of rows, which share a 256-byte line of banks).
 // * Softmax in f32 with base-2 exponents: p = 2^(c s - m), c = scale * log2 e
 //   folded into one FMA; m lags (kLag).  Weights are rounded to the 16-bit
 //   type for the second product, the sum is taken of the unrounded ones.
 // * Masks are applied only in blocks that some row does not wholly see, by
-//   selects on scores; V of slots that are not there is zeroed on the way to
-//   LDS, and non-finite V of a token that some rows see and others do not is
-//   kept away from the latter (see `special`).
+//   selects on scores.  In those blocks a pass over V in LDS zeroes slots that
+//   are not there and non-finite values (weight 0 times infinity is not 0);
+//   the latter are added to the rows that see them afterwards, one by one.
+//   Such blocks run in a loop of their own, so that the common one is small
+//   and keeps its accumulators in place.
+
+#include <type_traits>
 
 #include "attention_common.hpp"
 
@@ -39,10 +46,9 @@ static_assert(R == 128 && B == 64, "four waves of 32 rows, blocks of two 32-key 
 
 template <int D>
 struct Lds {
-  static constexpr int kKRow = D * 2 + 16;   // bytes of a padded K row
-  static constexpr int kVRow = D * 2;
-  static constexpr int kV = B * kKRow;       // offset of V in a buffer
-  static constexpr int kSize = kV + B * kVRow;
+  static constexpr int kRow = D * 2;         // bytes
+  static constexpr int kV = B * kRow;        // offset of V in a buffer
+  static constexpr int kSize = 2 * kV;
 };
 
 template <bool kBf16, int D>
@@ -51,8 +57,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
   constexpr int KS = D / 16;            // k steps of the first product
   constexpr int DT = D / 32;            // 32-column tiles of the output
   constexpr int CPR = D / 8;            // 16-byte chunks per row
-  constexpr int RPL = 256 / CPR;        // rows per pass of the 256 threads' loads
-  constexpr int NL = B / RPL;           // passes
+  constexpr int RPW = 64 / CPR;         // rows per direct load of a wave
+  constexpr int NL = B / RPW / 4;       // direct loads per wave, block and tensor
   __shared__ __attribute__((aligned(256))) char buf[2][L::kSize];
   __shared__ uint32_t flags[2][4];      // per buffer and wave: V holds non-finite values
   extern __shared__ char dyn[];
@@ -88,7 +94,6 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     if (!direct_tile<R>(p, tiles_bound - 1 - wg % tiles_bound, lane, seq, tile_in_seq)) return;
   }
 
-  bool first_piece = true;
   while (unit < end) {
     uint32_t b0 = 0;
     if (split) {
@@ -105,7 +110,6 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     const uint32_t whole = b1;
     if (split && b1 - b0 > end - unit) b1 = b0 + (end - unit);
     const bool complete = b0 == 0 && b1 == whole;
-    if (!first_piece) __syncthreads();   // the previous piece's last block is no longer read
 
     // ---- this lane's row ----
     const uint32_t r = wave * 32 + l32 < t.rows ? wave * 32 + l32 : t.rows - 1;
@@ -142,40 +146,59 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       const int32_t k = key0_of(i) + (int32_t)lane;
       return i < nblk && k < t.hi ? slot_of(kv, t.seq, k) : -1;
     };
-    u32x4 kr[NL], vr[NL];
-    const uint32_t lrow = tid / CPR, lch = tid % CPR;   // this thread's row and chunk of a pass
-    auto fetch = [&](int32_t slot) {
+    // The wave's share of the block's rows to LDS: load n covers rows (4 n + wave) RPW ..
+    const uint32_t lrow = lane / CPR, lch = lane % CPR;
+    const bool shared_page = kv.page.d % RPW == 0;
+    auto kswz = [](uint32_t row) { return D == 128 ? (row & 15) : ((row >> 1) & 7); };            // of a 16-byte chunk
+    auto vswz = [](uint32_t row) { return (D == 128 ? (row & 3) : ((row >> 1) & 1)) * 4; };
+    auto fetch = [&](uint32_t buffer, int32_t slot) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int32_t s = __shfl(slot, (int)(i * RPL + lrow));
-        const size_t at = (size_t)(s < 0 ? 0 : s) * row_elems + head * D + lch * 8;
-        kr[i] = *reinterpret_cast<const u32x4*>(kv.k + at);
-        vr[i] = *reinterpret_cast<const u32x4*>(kv.v + at);
+      for (int n = 0; n < NL; ++n) {
+        const uint32_t row0 = (4 * n + wave) * RPW, row = row0 + lrow;
+        char* const kl = buf[buffer] + row0 * L::kRow;
+        const uint32_t koff = (lch ^ kswz(row)) * 16, voff = (lch ^ vswz(row)) * 16;
+        if (shared_page) {
+          // keys past t.hi or of an absent page share their first key's fate or lie in its page: valid memory
+          const int32_t s0 = __builtin_amdgcn_readlane(slot, (int)row0);
+          const size_t at = ((size_t)(s0 < 0 ? 0 : s0) * row_elems + head * D) * 2;
+          const uint32_t lane_off = lrow * (uint32_t)(row_elems * 2);
+          dma16(reinterpret_cast<const char*>(kv.k) + at, lane_off + koff, kl);
+          dma16(reinterpret_cast<const char*>(kv.v) + at, lane_off + voff, kl + L::kV);
+        } else {
+#pragma unroll 1
+          for (uint32_t j = 0; j < (uint32_t)RPW; ++j) {
+            const int32_t s0 = __builtin_amdgcn_readlane(slot, (int)(row0 + j));
+            const size_t at = ((size_t)(s0 < 0 ? 0 : s0) * row_elems + head * D) * 2;
+            if (lrow == j) {
+              dma16(reinterpret_cast<const char*>(kv.k) + at, koff, kl);
+              dma16(reinterpret_cast<const char*>(kv.v) + at, voff, kl + L::kV);
+            }
+          }
+        }
       }
     };
-    // the block's rows to LDS; V of absent slots as zeros
-    auto store = [&](uint32_t buffer, int32_t slot, uint64_t live, bool edge) {
-      if (~live) {
+    // zeroes V of absent slots and non-finite values; notes whether there are any of the latter
+    auto fix_v = [&](uint32_t buffer, uint64_t live) {
+      bool special = false;
+      char* const vl = buf[buffer] + L::kV;
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-          if (__shfl(slot, (int)(i * RPL + lrow)) < 0) vr[i] = u32x4{0, 0, 0, 0};
+      for (int n = 0; n < NL; ++n) {
+        const uint32_t at = (n * 256 + tid) * 16, row = at / L::kRow;
+        u32x4 v = *reinterpret_cast<const u32x4*>(vl + at);
+        const bool there = (live >> row) & 1;
+        bool change = !there;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool sp = any_special<kBf16>(v[e]);
+          special |= there && sp;
+          change |= sp;
+          v[e] = there ? finite_only<kBf16>(v[e]) : 0u;
+        }
+        if (change) *reinterpret_cast<u32x4*>(vl + at) = v;
       }
-      if (edge) {
-        bool special = false;
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) special |= any_special<kBf16>(vr[i][e]);
-        flags[buffer][wave] = __ballot(special) != 0;
-      }
-      char* const b = buf[buffer];
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint32_t row = i * RPL + lrow;
-        *reinterpret_cast<u32x4*>(b + row * L::kKRow + lch * 16) = kr[i];
-        const uint32_t swz = D == 128 ? (row & 3) : ((row >> 1) & 1);
-        *reinterpret_cast<u32x4*>(b + L::kV + row * L::kVRow + ((lch * 16) ^ (swz * 64))) = vr[i];
-      }
+      flags[buffer][wave] = __ballot(special) != 0;
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      return (flags[buffer][0] | flags[buffer][1] | flags[buffer][2] | flags[buffer][3]) != 0;
     };
     // some row of the tile does not see some key of the block that starts at key0
     auto edge_of = [&](int32_t key0) {
@@ -184,35 +207,36 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 
     int32_t slot = slots(0), slot_next = slots(1);
     uint64_t live = __ballot(slot >= 0);
-    if (nblk) {
-      if (live) fetch(slot);
-      store(0, slot, live, edge_of(key0_of(0)));
-    }
-    __syncthreads();
+    if (live) fetch(0, slot);
+    wait_vm_barrier<0>();
 
-    for (uint32_t i = 0; i < nblk; ++i) {
+    // One block.  kEdge: some row does not see some key (of the tile's rows: the choice is the workgroup's).
+    auto block = [&](auto edge_tag, uint32_t i) {
+      constexpr bool kEdge = decltype(edge_tag)::value;
       const int32_t key0 = key0_of(i);
       const char* const kb = buf[i & 1];
       const char* const vb = kb + L::kV;
       const uint64_t live_next = __ballot(slot_next >= 0);
-      if (live_next) fetch(slot_next);
+      if (live_next) fetch((i + 1) & 1, slot_next);
       const int32_t slot_after = slots(i + 2);
+      bool special = false;
+      if constexpr (kEdge) special = fix_v(i & 1, live);
 
       // does any of the wave's rows see any of the block's keys?
-      if (live && key0 <= wpos1) {
+      if (!kEdge || (live && key0 <= wpos1)) {
         floatx16 s[2];
-        const char* const kl = kb + l32 * L::kKRow + h * 16;
+        const uint32_t kbase = l32 * L::kRow, kx = (h ^ kswz(l32)) * 16;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[st][e] = 0.f;
 #pragma unroll
           for (int k = 0; k < KS; ++k)
-            s[st] = mfma32<kBf16>(*reinterpret_cast<const short8_t*>(kl + st * 32 * L::kKRow + k * 32), q[k], s[st]);
+            s[st] = mfma32<kBf16>(
+                *reinterpret_cast<const short8_t*>(kb + st * 32 * L::kRow + (kbase + (kx ^ (k * 32)))), q[k], s[st]);
         }
         // element e of tile st is key 32 st + 8 (e / 4) + 4 h + e % 4
-        const bool edge = key0 + (int32_t)B - 1 > wpos0 || (p.window && key0 <= wfloor1 && key0 + (int32_t)B > sinks);
-        if (edge || ~live) {
+        if constexpr (kEdge) {
           const uint32_t lo32 = (uint32_t)(live >> (4 * h)), hi32 = (uint32_t)(live >> (32 + 4 * h));
 #pragma unroll
           for (int st = 0; st < 2; ++st)
@@ -257,49 +281,52 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
           }
         // V^T fragment of k step ks, columns 32 d ..: keys 16 ks + 4 h + (0..3), and 8 further on
         const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
-        const uint32_t vswz = (D == 128 ? (vrow & 3) : ((vrow >> 1) & 1)) * 64;
-        const uint32_t vcol = (lane & 16) * 2 + (lane & 3) * 8;
+        const uint32_t vx = ((lane & 16) * 2 + (lane & 3) * 8) ^ (vswz(vrow) * 16);
         auto vfrag = [&](int ks, int d) {
-          const char* const a = vb + vrow * L::kVRow + ks * 16 * L::kVRow + ((d * 64 + vcol) ^ vswz);
-          return join(read_tr(a), read_tr(a + 8 * L::kVRow));
+          const char* const a = vb + ks * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
+          return join(read_tr(a), read_tr(a + 8 * L::kRow));
         };
-        const bool special = edge_of(key0) && (flags[i & 1][0] | flags[i & 1][1] | flags[i & 1][2] | flags[i & 1][3]);
-        if (!special) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vfrag(ks, d), w[ks], o[d]);
-        } else {
-          // Weight 0 times a non-finite V is not 0: the finite values go through the product, the others are counted
-          // per row over the keys it sees, and put in where the count is not zero.
-          constexpr short one = kBf16 ? 0x3F80 : 0x3C00;
-          short8_t sees[4];
+          for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vfrag(ks, d), w[ks], o[d]);
+        if constexpr (kEdge) {
+          if (special) {
+            // the non-finite values of the block, from the cache, to the rows that see their key
+            typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
+            const u32x16 wv = __builtin_bit_cast(u32x16, w);
+#pragma unroll 1
+            for (int j = 0; j < (int)B; ++j) {      // key j: an element of half (j / 4) % 2
+              const int32_t sj = __builtin_amdgcn_readlane(slot, j);
+              const int in32 = j & 31, half = (in32 >> 2) & 1, e = 4 * (in32 >> 3) + (in32 & 3);
+              const uint32_t pair = wv[8 * (j >> 5) + (e >> 1)];
+              const uint32_t pw = __shfl(e & 1 ? pair >> 16 : pair & 0xFFFFu, (int)l32 + 32 * half);
+              const float x = to_f32<kBf16>((uint16_t)pw);
+              if (sj < 0) continue;
+              const uint16_t* const row = kv.v + (size_t)sj * row_elems + head * D + 4 * h;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+              for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sees[ks][e] = s[ks >> 1][8 * (ks & 1) + e] == -INFINITY ? (short)0 : one;
+                for (int k = 0; k < 4; ++k) {
+                  const u32x2 v = *reinterpret_cast<const u32x2*>(row + d * 32 + k * 8);
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            floatx16 nan, inf, neg;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) nan[e] = inf[e] = neg[e] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const Special<kBf16> v(vfrag(ks, d));
-              o[d] = mfma32<kBf16>(v.fin, w[ks], o[d]);
-              nan = mfma32<kBf16>(v.nan, sees[ks], nan);
-              inf = mfma32<kBf16>(v.pos, sees[ks], inf);
-              neg = mfma32<kBf16>(v.neg, sees[ks], neg);
+                  for (int y = 0; y < 4; ++y) {
+                    const float vf = to_f32<kBf16>((uint16_t)(v[y >> 1] >> (16 * (y & 1))));
+                    o[d][4 * k + y] += x != 0.f && !(fabsf(vf) < INFINITY) ? x * vf : 0.f;
+                  }
+                }
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[d][e] = with_special(o[d][e], nan[e], inf[e], neg[e]);
           }
         }
       }
-      if (i + 1 < nblk) store((i + 1) & 1, slot_next, live_next, edge_of(key0_of(i + 1)));
+      slot = slot_next;
       slot_next = slot_after;
       live = live_next;
-      __syncthreads();
+      wait_vm_barrier<0>();   // the next block is in place, this one no longer read
+    };
+    for (uint32_t i = 0; i < nblk;) {
+      for (; i < nblk && (edge_of(key0_of(i)) || ~live); ++i) block(std::true_type{}, i);
+      for (; i < nblk && !(edge_of(key0_of(i)) || ~live); ++i) block(std::false_type{}, i);
     }
 
     // ---- the piece's result ----
@@ -340,7 +367,6 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     }
     unit += split ? b1 - b0 : 1;
     ++tile;
-    first_piece = false;
   }
 }
 
