@@ -94,6 +94,26 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_fast = None
+
+
+def _quick():
+    """csrc/torch_binding.cpp, bound to the loaded library: the short way of ordinary calls.  It returns None for
+    anything it does not take, which then goes through the checks below.  False where it was never built."""
+    global _fast
+    if _fast is None:
+        L = lib()
+        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")):
+            _fast = False
+        else:
+            import torch  # noqa: F401  (its libraries come first)
+            from . import _binding as b
+            b.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.kaio_linear_w4a16, L.kaio_rope_append, L.kaio_paged_attention, L.kaio_paged_attention_workspace_size)])
+            _fast = b
+    return _fast
+
+
 def kaio_last_error() -> str:
     return lib().kaio_last_error().decode()
 
@@ -120,6 +140,17 @@ def _stream(device, stream):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _allocate(device, stream, make):
+    """make() with ``stream`` (if given) current, so that the memory it allocates belongs to the stream that uses it."""
+    if stream is None:
+        return make()
+    import torch
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    with torch.cuda.stream(s):
+        return make()
 
 
 def _tensor(t, name, dtypes, device=None, rank=2, any_offset=False):
@@ -277,6 +308,11 @@ def kaio_linear_w4a16(x, w, s, bias=None, activation="none", residual=None, y=No
     x f16[M,K]; w packed INT4 as int32/uint32 [K/8, N]; s f16[K/128, N]; bias f16[N]; residual f16[M, N];
     activation one of ACTIVATION_CODES.  ``y`` may be ``residual`` itself (updated in place).
     """
+    fast = _fast or _quick()
+    if fast and stream is None:
+        r = fast.linear(x, w, s, bias, ACTIVATION_CODES.get(activation, -1), residual, y)
+        if r is not None:
+            return r
     import torch
     f16 = (torch.float16,)
     _tensor(x, "x", f16, any_offset=True)
@@ -298,7 +334,7 @@ def kaio_linear_w4a16(x, w, s, bias=None, activation="none", residual=None, y=No
         if bias.shape[0] != N:
             raise ValueError(f"bias must be [{N}], got {list(bias.shape)}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=dev)
+        y = _allocate(dev, stream, lambda: torch.empty((M, N), dtype=torch.float16, device=dev))
     for t, n in ((residual, "residual"), (y, "y")):
         if t is not None:
             _tensor(t, n, f16, dev, any_offset=True)
@@ -351,6 +387,8 @@ class KaioPagedKV:
                            lens.data_ptr(), 2 if self.dtype == torch.float16 else 1, *k_cache.shape, seqs,
                            page_table.shape[1])
         self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
+        self._index = dev.index
 
     def _heads(self, t, name, heads=None):
         _tensor(t, name, (self.dtype,), self.device, rank=3, any_offset=True)
@@ -374,8 +412,13 @@ def kaio_rope_append(q, k, v, positions, inv_freq, sections, paged, interleaved=
     elements past 2 * pairs of a head pass through).  Pair j is elements (2j, 2j+1) when ``interleaved``, else
     (j, j + pairs).  ``q_out`` may be ``q`` itself (turned in place).
     """
-    import torch
     p = _paged(paged)
+    fast = _fast or _quick()
+    if fast and stream is None:
+        r = fast.rope_append(q, k, v, positions, inv_freq, sections, p._addr, p._index, bool(interleaved), q_out)
+        if r is not None:
+            return r
+    import torch
     p._heads(q, "q")
     T = q.shape[0]
     p._heads(k, "k", p.kv_heads)
@@ -390,7 +433,7 @@ def kaio_rope_append(q, k, v, positions, inv_freq, sections, paged, interleaved=
     if min(sections, default=0) < 0 or sum(sections) != inv_freq.shape[0]:
         raise ValueError(f"sections {list(sections)} must be counts that add up to the {inv_freq.shape[0]} pairs of inv_freq")
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _allocate(p.device, stream, lambda: torch.empty_like(q))
     p._heads(q_out, "q_out")
     if q_out.shape != q.shape:
         raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
@@ -410,14 +453,19 @@ def kaio_paged_attention(q, paged, max_new, scale, window=0, sinks=0, out=None, 
     above p - window and the first ``sinks``.  A row that sees nothing is zero.  ``workspace`` (uint8) is
     allocated here when it is needed and not given.
     """
-    import torch
     p = _paged(paged)
+    fast = _fast or _quick()
+    if fast and stream is None:
+        r = fast.attention(q, p._addr, p._index, max_new, scale, window, sinks, out, workspace)
+        if r is not None:
+            return r
+    import torch
     p._heads(q, "q")
     T, hq, _ = q.shape
     if hq % p.kv_heads:
         raise ValueError(f"q has {hq} heads, not a multiple of the cache's {p.kv_heads}")
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocate(p.device, stream, lambda: torch.empty_like(q))
     p._heads(out, "out")
     if out.shape != q.shape:
         raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
@@ -425,7 +473,7 @@ def kaio_paged_attention(q, paged, max_new, scale, window=0, sinks=0, out=None, 
         raise ValueError("max_new, window and sinks must be counts that fit in i32")
     need = lib().kaio_paged_attention_workspace_size(p._ref, T, hq, max_new)
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=p.device)
+        workspace = _allocate(p.device, stream, lambda: torch.empty((need,), dtype=torch.uint8, device=p.device))
     if workspace is not None:
         _tensor(workspace, "workspace", (torch.uint8,), p.device, rank=1, any_offset=True)
     _check(lib().kaio_paged_attention(p._ref, q.data_ptr(), out.data_ptr(), T, hq, max_new, scale, window, sinks,

@@ -32,6 +32,10 @@ SOURCES = ["kaio_abi.cpp", "qkv_prefill.hip", "qkv_decode.hip", "gemm_f16f32.hip
 ROOF_LIB = os.path.join(PKG, "libkaio_roof.so")
 ROOF_SOURCES = ["roof.hip"]
 
+# the Python call path of the serving operators (host code, against torch's headers)
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = "torch_binding.cpp"
+
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -97,17 +101,40 @@ def build_host_sanitized(verbose: bool = False) -> str:
     return lib
 
 
+def build_binding() -> str:
+    """_binding.so: csrc/torch_binding.cpp by the host compiler."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include")]
+    libs = os.path.join(root, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc],
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-lc10_hip", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SOURCE}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(extra_flags=(), verbose: bool = False) -> str:
     """Compile every source for gfx950, link libkaio.so (and the benchmark's
-    libkaio_roof.so); returns the path of libkaio.so."""
+    libkaio_roof.so) and the Python binding; returns the path of libkaio.so."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = SOURCES + ROOF_SOURCES
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(lambda s: _compile(s, list(extra_flags)), srcs))
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], ROOF_LIB)
+    binding.result()
     if verbose:
-        print(f"built {LIB} and {ROOF_LIB}")
+        print(f"built {LIB}, {ROOF_LIB} and {BINDING}")
     return LIB
 
 

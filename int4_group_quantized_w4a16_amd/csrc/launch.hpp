@@ -151,8 +151,62 @@ struct LinearProblem {
   uint32_t m, n, k;
   int act;                    // kaio_activation
 };
-// workgroups of a call
-constexpr uint64_t linear_wgs(uint64_t m, uint64_t n) { return (m + 15) / 16 * ((n + 15) / 16); }
+// Forms of the linear product.  Strips (the split-K kernel): 16 * vec columns
+// per workgroup and up to `rows` rows.  Tiles: `waves` waves per set, `rows`
+// rows, `sets` sets of waves that share out the groups, and `blocks` blocks of
+// 16 * waves columns per workgroup.
+struct LinearForm {
+  uint32_t vec, waves, rows, sets, blocks;   // vec 0: a tile
+  constexpr uint32_t code() const { return (((vec * 32 + waves) * 256 + rows) * 8 + sets) * 8 + blocks; }
+};
+// Strips.  n = 4096 / 11008, k = 4096, us with weights streamed from HBM, by
+// columns per strip (16, 32, 64): m = 8 6.4 5.9 7.0 / 14.3 10.4 8.1, m = 16
+// 7.4 6.9 8.0 / 19.1 13.1 9.6, m = 32 9.8 10.0 12.3 / - 18.7 13.5, m = 64 11.8
+// 13.2 17.6 / - 31.4 21.5: the widest strip that still gives one workgroup to
+// every compute unit, and 32 columns at least up to m = 16.
+constexpr LinearForm linear_strips(uint32_t m, uint32_t n) {
+  const uint32_t rows = m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  if (n > 8192) return LinearForm{4, m <= 16 ? 16u : 8u, rows, 1, 1};
+  const bool narrow = n % 2 != 0 || (m > 16 && n <= 4096);
+  return LinearForm{narrow ? 1u : 2u, m <= 16 ? 16u : 8u, rows, 1, 1};
+}
+// Tiles: as prefill_cost, `cost` is the time of a full pass at k = 4096 (0.1
+// us, epilogue with bias, silu and residual) over slots = 256 x the
+// workgroups a compute unit holds at once; a partial pass takes base + (1 -
+// base) x its share.  The set counts divide the groups.
+struct LinearFormCost {
+  LinearForm f;
+  uint32_t slots, cost, base;
+};
+constexpr LinearFormCost kLinearForms[] = {
+    {{0, 4, 64, 4, 1}, 256, 153, 850},  {{0, 4, 64, 2, 1}, 256, 162, 850},  {{0, 4, 96, 2, 1}, 256, 201, 850},
+    {{0, 4, 64, 2, 2}, 256, 233, 850},  {{0, 4, 96, 2, 2}, 256, 293, 800},
+    {{0, 4, 128, 2, 2}, 256, 356, 800}, {{0, 8, 96, 1, 2}, 256, 503, 750},  {{0, 8, 128, 1, 2}, 256, 635, 750},
+    {{0, 8, 128, 1, 3}, 256, 860, 750}, {{0, 4, 64, 1, 1}, 768, 376, 450},  {{0, 4, 64, 1, 2}, 512, 433, 450},
+    {{0, 4, 96, 1, 1}, 512, 368, 500}};
+constexpr uint64_t linear_tiles(LinearForm f, uint64_t m, uint64_t n) {
+  const uint64_t bn = 16 * f.waves * f.blocks;
+  return (m + f.rows - 1) / f.rows * ((n + bn - 1) / bn);
+}
+constexpr LinearForm linear_form(uint32_t m, uint32_t n, uint32_t k) {
+  const uint32_t groups = k / 128;
+  // up to 32 rows strips always; to 64 where they are faster than the four-set tile or there is none
+  if (m <= 32 || (m <= 64 && (n <= 4096 || (n <= 8192 && groups % 4 != 0)))) return linear_strips(m, n);
+  LinearForm best = kLinearForms[0].f;
+  uint64_t best_cost = ~0ull;
+  for (const LinearFormCost& c : kLinearForms) {
+    if (groups % c.f.sets != 0) continue;
+    const uint64_t wgs = linear_tiles(c.f, m, n), full = wgs / c.slots, rem = wgs % c.slots;
+    const uint64_t t = c.cost * (1000 * full + (rem ? c.base + (1000 - c.base) * rem / c.slots : 0));
+    if (t < best_cost) {
+      best_cost = t;
+      best = c.f;
+    }
+  }
+  return best;
+}
+// a bound on the workgroups of a call in any form (16 columns x 64 rows are the smallest tile)
+constexpr uint64_t linear_wgs(uint64_t m, uint64_t n) { return (m + 63) / 64 * ((n + 15) / 16); }
 hipError_t launch_linear_w4a16(const LinearProblem& p, hipStream_t stream);
 
 constexpr uint32_t kMaxAxes = 8;
