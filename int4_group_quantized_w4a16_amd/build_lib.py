@@ -26,7 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkaio.so")
 SOURCES = ["kaio_abi.cpp", "qkv_prefill.hip", "qkv_decode.hip", "gemm_f16f32.hip", "dequant_group_bwd.hip",
-           "linear_w4a16.hip", "rope_append.hip", "attention_rows.hip", "attention_stream.hip",
+           "linear_w4a16.hip", "rope_append.hip", "attention_rows.hip", "attention_stream.hip", "attention_join.hip",
            "attention_tile.hip"]
 # measurement aid for the benchmark (a plain streaming read), a library of its own
 ROOF_LIB = os.path.join(PKG, "libkaio_roof.so")

@@ -123,13 +123,15 @@ __device__ __forceinline__ short8_t join(short4_t a, short4_t b) {
   return short8_t{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// Partial results: per slot R rows of D f32, then R maxima, then R sums.
+// Workspace: a note per workgroup, then the partial results, per slot R rows
+// of D f32, R maxima and R sums.
 template <uint32_t R, uint32_t D>
-__device__ __forceinline__ float* partial_of(const PagedAttention& p, uint32_t slot) {
-  return static_cast<float*>(p.workspace) + (size_t)slot * (R * (D + 2));
+__device__ __forceinline__ float* partial_of(const PagedAttention& p, uint32_t workers, uint32_t slot) {
+  return reinterpret_cast<float*>(static_cast<JoinNote*>(p.workspace) + workers) + (size_t)slot * (R * (D + 2));
 }
 
-// Zeros for the rows of q that no sequence has: before q_start[0] and from q_start[seqs] on.
+// Zeros for the rows of q that no sequence has: before q_start[0] and from
+// q_start[seqs] on.  (At a kernel's end, where its loads wait for nobody.)
 __device__ __forceinline__ void zero_unowned(const PagedAttention& p, uint32_t wg, uint32_t wgs) {
   const uint32_t T = p.kv.tokens;
   const uint32_t a = p.kv.seqs ? (uint32_t)clamp_row(p.kv.q_start[0], T) : T;

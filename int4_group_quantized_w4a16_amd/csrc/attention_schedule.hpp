@@ -17,21 +17,23 @@
 // lengths may differ as they like.  A tile inside one part is finished there;
 // a part's first piece (of a tile begun earlier) and its last (of a tile that
 // goes on) are partial results -- running maximum, sum and unnormalized
-// output in f32 -- in the workspace, slots 2w and 2w + 1 of workgroup w, and a
-// second kernel joins each tile's pieces in order.  The lengths are only known
-// on the device, so every workgroup derives the line from them by itself.
+// output in f32 -- in the workspace, slots 2w and 2w + 1 of workgroup w.  The
+// workgroup that begins a tile it does not finish notes the tile and how many
+// workgroups go on with it, and a second kernel joins the pieces in order.
+// The lengths are only known on the device, so every workgroup derives the
+// line from them by itself (2 us; it needs one load of each array).
 //
 // Direct form, for calls with so many tiles that they balance by themselves:
 // one workgroup per tile and K/V head, nothing to join.
 #pragma once
 
+#include "common.hpp"
 #include "launch.hpp"
 #include "paged.hpp"
 
 namespace kaio {
 
 struct Tile {
-  uint32_t seq;
   uint32_t row0, rows;      // packed rows of the sequence
   int32_t q0;               // row of q of the sequence's first new token
   int32_t p0, p1;           // positions of the tile's first and last row
@@ -40,36 +42,33 @@ struct Tile {
   uint32_t ns, wb0, count;  // blocks: ns from 0, then from wb0
 };
 
+// A sequence's rows of q, [a, a + n) (inside q whatever q_start holds), and shift.
+struct Seq {
+  int32_t a, n, shift;
+};
 __device__ __forceinline__ int32_t clamp_row(int32_t x, uint32_t tokens) {
   return x < 0 ? 0 : x > (int32_t)tokens ? (int32_t)tokens : x;
 }
-// rows of q of sequence s (all of them inside q whatever q_start holds)
-__device__ __forceinline__ void seq_rows(const PagedKV& kv, uint32_t s, int32_t& a, int32_t& b) {
-  a = clamp_row(kv.q_start[s], kv.tokens);
-  b = clamp_row(kv.q_start[s + 1], kv.tokens);
-  if (b < a) b = a;
+__device__ __forceinline__ Seq seq_of(const PagedKV& kv, uint32_t s) {
+  const int32_t lo = kv.q_start[s], hi = kv.q_start[s + 1], len = kv.lens[s];
+  const int32_t a = clamp_row(lo, kv.tokens), b = clamp_row(hi, kv.tokens);
+  return Seq{a, b > a ? b - a : 0, (len > 0 ? len : 0) - hi};
 }
 template <uint32_t R>
-__device__ __forceinline__ uint32_t seq_tiles(const PagedAttention& p, uint32_t s) {
-  int32_t a, b;
-  seq_rows(p.kv, s, a, b);
-  return ((uint32_t)(b - a) * p.group.d + R - 1) / R;
+__device__ __forceinline__ uint32_t seq_tiles(const PagedAttention& p, const Seq& q) {
+  return ((uint32_t)q.n * p.group.d + R - 1) / R;
 }
 
 template <uint32_t R, uint32_t B>
-__device__ __forceinline__ Tile tile_info(const PagedAttention& p, uint32_t s, uint32_t i) {
+__device__ __forceinline__ Tile tile_info(const PagedAttention& p, const Seq& q, uint32_t i) {
   Tile t;
-  int32_t a, b;
-  seq_rows(p.kv, s, a, b);
-  const uint32_t g = p.group.d, rows = (uint32_t)(b - a) * g;
-  const int32_t len = p.kv.lens[s] > 0 ? p.kv.lens[s] : 0;
-  t.seq = s;
-  t.q0 = a;
+  const uint32_t rows = (uint32_t)q.n * p.group.d;
+  t.q0 = q.a;
   t.row0 = i * R;
   t.rows = rows - t.row0 < R ? rows - t.row0 : R;
-  t.shift = len - p.kv.q_start[s + 1];
-  t.p0 = a + (int32_t)p.group.div(t.row0) + t.shift;
-  t.p1 = a + (int32_t)p.group.div(t.row0 + t.rows - 1) + t.shift;
+  t.shift = q.shift;
+  t.p0 = q.a + (int32_t)p.group.div(t.row0) + t.shift;
+  t.p1 = q.a + (int32_t)p.group.div(t.row0 + t.rows - 1) + t.shift;
   t.hi = t.p1 < (int32_t)p.kv.cap ? t.p1 + 1 : (int32_t)p.kv.cap;
   t.ns = t.wb0 = t.count = 0;
   if (t.hi <= 0) {
@@ -105,7 +104,7 @@ __device__ __forceinline__ bool direct_tile(const PagedAttention& p, uint32_t in
   uint32_t base = 0;
   for (uint32_t s0 = 0; s0 < p.kv.seqs; s0 += 64) {
     const uint32_t s = s0 + lane;
-    uint32_t n = s < p.kv.seqs ? seq_tiles<R>(p, s) : 0, end = n;
+    uint32_t n = s < p.kv.seqs ? seq_tiles<R>(p, seq_of(p.kv, s)) : 0, end = n;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) {
       const uint32_t o = __shfl_up(end, x);
@@ -130,6 +129,7 @@ constexpr uint32_t kSchedPer = kSchedTiles / kSchedThreads;
 struct Line {
   uint32_t first[kSchedTiles + 1];   // first tile of each sequence
   uint32_t start[kSchedTiles + 1];   // first unit of each tile
+  Seq seq[kSchedTiles];
   uint32_t wave_sum[kSchedThreads / 64];
 };
 
@@ -179,7 +179,11 @@ __device__ __forceinline__ uint32_t build_line(const PagedAttention& p, Line& li
 #pragma unroll
   for (uint32_t k = 0; k < kSchedPer; ++k) {
     const uint32_t s = tid * kSchedPer + k;
-    v[k] = s < n ? seq_tiles<R>(p, s) : 0;
+    v[k] = 0;
+    if (s < n) {
+      line.seq[s] = seq_of(p.kv, s);
+      v[k] = seq_tiles<R>(p, line.seq[s]);
+    }
   }
   block_scan(v, n, line.first, line.wave_sum);
   // overlapping sequences (q_start not ascending) could have more tiles than rows: those past the bound are dropped
@@ -190,7 +194,7 @@ __device__ __forceinline__ uint32_t build_line(const PagedAttention& p, Line& li
     v[k] = 0;
     if (i < tiles) {
       const uint32_t s = part_of(line.first, n, i);
-      v[k] = units_of(tile_info<R, B>(p, s, i - line.first[s]));
+      v[k] = units_of(tile_info<R, B>(p, line.seq[s], i - line.first[s]));
     }
   }
   block_scan(v, tiles, line.start, line.wave_sum);
@@ -215,5 +219,90 @@ __device__ __forceinline__ Cut cut_of(uint32_t total, uint32_t workers) {
   const uint32_t per = total / parts;
   return Cut{per, total - per * parts};
 }
+
+// What a workgroup notes of a tile that it begins and others go on with.
+struct JoinNote {
+  uint32_t more;     // workgroups after it with a piece of the tile (0: no such tile)
+  uint32_t head;
+  int32_t q0;
+  uint32_t row0, rows, pad[3];
+};
+
+// The pieces of one workgroup, in order.
+template <uint32_t R, uint32_t B, uint32_t kMinUnits>
+struct Walk {
+  const PagedAttention& p;
+  Line& line;             // split form only
+  const bool split;
+  uint32_t wg, unit = 0, end = 0, total = 0, tiles = 0, tile = 0;
+  uint32_t head = 0;
+  Cut cut{0, 0};
+  uint32_t seq_index = 0; // the piece's sequence
+  Seq seq{};              // direct form: the same,
+  uint32_t direct = 0;    // and the tile within it
+  JoinNote note{};
+
+  // the current piece: blocks b0 .. b1-1 of tile t; complete: all of it
+  Tile t;
+  uint32_t b0 = 0, b1 = 0;
+  bool complete = true;
+
+  // split form: every thread of the workgroup (barriers inside)
+  __device__ __forceinline__ Walk(const PagedAttention& p_, Line& line_, bool split_, uint32_t tiles_bound, uint32_t lane)
+      : p(p_), line(line_), split(split_), wg(xcd_remap(blockIdx.x, gridDim.x)) {
+    if (split) {
+      tiles = build_line<R, B>(p, line);
+      total = line.start[tiles];
+      if (tiles == 0) return;
+      const uint32_t all = total * p.kv.kv_heads;
+      cut = cut_of<kMinUnits>(all, gridDim.x);
+      unit = cut.start(wg);
+      end = cut.start(wg + 1);
+      if (end > all) end = all;
+      if (unit >= end) return;
+      head = unit / total;
+      tile = part_of(line.start, tiles, unit - head * total);
+    } else {
+      uint32_t s;
+      head = wg / tiles_bound;
+      // later tiles see more keys: they start first
+      if (direct_tile<R>(p, tiles_bound - 1 - wg % tiles_bound, lane, s, direct)) {
+        seq = seq_of(p.kv, s);
+        seq_index = s;
+        end = 1;
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool next() {
+    if (unit >= end) return false;
+    if (split) {
+      if (tile == tiles) {
+        tile = 0;
+        ++head;
+      }
+      seq_index = part_of(line.first, p.kv.seqs, tile);
+      b0 = unit - head * total - line.start[tile];
+      t = tile_info<R, B>(p, line.seq[seq_index], tile - line.first[seq_index]);
+      const uint32_t whole = units_of(t);
+      b1 = whole - b0 < end - unit ? whole : b0 + (end - unit);
+      complete = b0 == 0 && b1 == whole;
+      if (b0 == 0 && !complete) {
+        const uint32_t last = head * total + line.start[tile] + whole - 1;
+        note = JoinNote{cut.owner(last) - wg, head, t.q0, t.row0, t.rows, {}};
+      }
+      unit += b1 - b0;
+      ++tile;
+    } else {
+      t = tile_info<R, B>(p, seq, direct);
+      b1 = units_of(t);
+      unit = end;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void leave_note() const {
+    if (split && threadIdx.x == 0) static_cast<JoinNote*>(p.workspace)[wg] = note;
+  }
+};
 
 }  // namespace kaio

@@ -55,43 +55,12 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
   const bool negate = p.scale < 0.f;
   const float c = fmaxf(fabsf(p.scale) * 1.44269504088896341f, 1.17549435e-38f);
 
-  zero_unowned(p, blockIdx.x, gridDim.x);
-
-  uint32_t unit = 0, end = 1, total = 0, tiles = 0, head = 0, seq = 0, tile_in_seq = 0, tile = 0;
-  const uint32_t wg = xcd_remap(blockIdx.x, gridDim.x);
-  if (split) {
-    tiles = build_line<R, B>(p, line);
-    total = line.start[tiles];
-    if (tiles == 0) return;
-    const Cut cut = cut_of<kStreamMinUnits>(total * kv.kv_heads, gridDim.x);
-    unit = cut.start(wg);
-    end = cut.start(wg + 1);
-    if (end > total * kv.kv_heads) end = total * kv.kv_heads;
-    if (unit >= end) return;
-    head = unit / total;
-    tile = part_of(line.start, tiles, unit - head * total);
-  } else {
-    head = wg / tiles_bound;
-    if (!direct_tile<R>(p, tiles_bound - 1 - wg % tiles_bound, lane, seq, tile_in_seq)) return;
-  }
-
+  Walk<R, B, kStreamMinUnits> walk(p, line, split, tiles_bound, lane);
   bool first_piece = true;
-  while (unit < end) {
-    uint32_t b0 = 0;
-    if (split) {
-      if (tile == tiles) {
-        tile = 0;
-        ++head;
-      }
-      seq = part_of(line.first, kv.seqs, tile);
-      tile_in_seq = tile - line.first[seq];
-      b0 = unit - head * total - line.start[tile];
-    }
-    const Tile t = tile_info<R, B>(p, seq, tile_in_seq);
-    uint32_t b1 = units_of(t);
-    const uint32_t whole = b1;
-    if (split && b1 - b0 > end - unit) b1 = b0 + (end - unit);
-    const bool complete = b0 == 0 && b1 == whole;
+  while (walk.next()) {
+    const Tile& t = walk.t;
+    const uint32_t b0 = walk.b0, b1 = walk.b1, head = walk.head, seq = walk.seq_index;
+    const bool complete = walk.complete;
 
     const uint32_t r = l16 < t.rows ? l16 : t.rows - 1;
     const uint32_t pr = t.row0 + r, tok = p.group.div(pr);
@@ -118,7 +87,7 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
     };
     auto slots = [&](uint32_t i) {                  // slot of key lane % 32 of block i
       const int32_t k = key0_of(i) + (int32_t)(lane & 31);
-      return i < nblk && k < t.hi ? slot_of(kv, t.seq, k) : -1;
+      return i < nblk && k < t.hi ? slot_of(kv, seq, k) : -1;
     };
     u32x4 kr[NL], vr[NL];
     const uint32_t lrow = lane / CPR, lch = lane % CPR;
@@ -299,7 +268,7 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
         for (int e = 0; e < PT; e += 2) packed[e / 2] = pack2<kBf16>(acc[e] * inv, acc[e + 1] * inv);
         __builtin_memcpy(__builtin_assume_aligned(dst, PT * 2), packed, PT * 2);
       } else {
-        float* const part = partial_of<R, D>(p, 2 * wg + (b0 == 0));
+        float* const part = partial_of<R, D>(p, gridDim.x, 2 * walk.wg + (b0 == 0));
 #pragma unroll
         for (int e = 0; e < PT; e += 4)
           *reinterpret_cast<floatx4*>(part + row * D + col + e) = floatx4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
@@ -309,57 +278,10 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
         }
       }
     }
-    unit += split ? b1 - b0 : 1;
-    ++tile;
     first_piece = false;
   }
-}
-
-// Joins the pieces of the split tiles, in order: one workgroup per tile, K/V
-// head and 8 of its rows... each thread four columns of one row.
-template <bool kBf16, int D, uint32_t RT, uint32_t BT, uint32_t kMinUnits>
-__global__ void __launch_bounds__(256) attention_join_kernel(PagedAttention p, uint32_t workers, uint32_t tiles_bound) {
-  constexpr uint32_t TPR = D / 4;               // threads per row
-  constexpr uint32_t RPB = 256 / TPR;           // rows per workgroup
-  constexpr uint32_t GROUPS = RT / RPB ? RT / RPB : 1;
-  __shared__ Line line;
-  const uint32_t tid = threadIdx.x;
-  const uint32_t tiles = build_line<RT, BT>(p, line);
-  const uint32_t grp = blockIdx.x % GROUPS, tile = blockIdx.x / GROUPS % tiles_bound, head = blockIdx.x / GROUPS / tiles_bound;
-  if (tile >= tiles) return;
-  const uint32_t total = line.start[tiles];
-  const Cut cut = cut_of<kMinUnits>(total * p.kv.kv_heads, workers);
-  const uint32_t a = head * total + line.start[tile], b = head * total + line.start[tile + 1];
-  const uint32_t w0 = cut.owner(a), w1 = cut.owner(b - 1);
-  if (w0 == w1) return;                         // finished by its workgroup
-  const uint32_t seq = part_of(line.first, p.kv.seqs, tile);
-  const Tile t = tile_info<RT, BT>(p, seq, tile - line.first[seq]);
-  const uint32_t row = grp * RPB + tid / TPR, col = tid % TPR * 4;
-  if (row >= t.rows) return;
-  float m = -INFINITY, l = 0.f;
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (uint32_t w = w0; w <= w1; ++w) {
-    const float* const part = partial_of<RT, D>(p, 2 * w + (w == w0));
-    const floatx4 v = *reinterpret_cast<const floatx4*>(part + (size_t)row * D + col);
-    const float mw = part[RT * D + row], lw = part[RT * D + RT + row];
-    const float m1 = fmaxf(m, mw), base = m1 == -INFINITY ? 0.f : m1;
-    const float fo = exp2_fast(m - base), fw = exp2_fast(mw - base);
-    l = l * fo + lw * fw;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = acc[e] * fo + v[e] * fw;
-    m = m1;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const uint32_t pr = t.row0 + row, tok = p.group.div(pr), g = p.group.d;
-  uint16_t* const dst = p.out + ((size_t)(t.q0 + (int32_t)tok) * p.q_heads + head * g + (pr - tok * g)) * D + col;
-  *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<kBf16>(acc[0] * inv, acc[1] * inv), pack2<kBf16>(acc[2] * inv, acc[3] * inv)};
-}
-
-template <bool kBf16, int D, uint32_t RT, uint32_t BT, uint32_t kMinUnits>
-void launch_join(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream) {
-  constexpr uint32_t rpb = 256 / (D / 4), groups = RT / rpb ? RT / rpb : 1;
-  hipLaunchKernelGGL((attention_join_kernel<kBf16, D, RT, BT, kMinUnits>), dim3(plan.tiles * p.kv.kv_heads * groups),
-                     dim3(256), 0, stream, p, plan.workgroups, plan.tiles);
+  walk.leave_note();
+  zero_unowned(p, blockIdx.x, gridDim.x);
 }
 
 }  // namespace
@@ -377,19 +299,6 @@ hipError_t launch_attention_stream(const PagedAttention& p, const AttentionPlan&
     else KAIO_STREAM(false, 64);
   }
 #undef KAIO_STREAM
-  return hipGetLastError();
-}
-
-hipError_t launch_attention_join(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream) {
-#define KAIO_JOIN(BF, DIM)                                                                        \
-  if (plan.stream) launch_join<BF, DIM, kStreamRows, kStreamKeys, kStreamMinUnits>(p, plan, stream); \
-  else launch_join<BF, DIM, kTileRows, kTileKeys, kTileMinUnits>(p, plan, stream)
-  if (p.kv.head_dim == 128) {
-    if (p.bf16) { KAIO_JOIN(true, 128); } else { KAIO_JOIN(false, 128); }
-  } else {
-    if (p.bf16) { KAIO_JOIN(true, 64); } else { KAIO_JOIN(false, 64); }
-  }
-#undef KAIO_JOIN
   return hipGetLastError();
 }
 

@@ -72,44 +72,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
   const bool negate = p.scale < 0.f;
   const float c = fmaxf(fabsf(p.scale) * 1.44269504088896341f, 1.17549435e-38f);
 
-  zero_unowned(p, blockIdx.x, gridDim.x);
-
-  // what this workgroup does: one whole tile, or a part of the line
-  uint32_t unit = 0, end = 1, total = 0, tiles = 0, head = 0, seq = 0, tile_in_seq = 0, tile = 0;
-  const uint32_t wg = xcd_remap(blockIdx.x, gridDim.x);
-  if (split) {
-    tiles = build_line<R, B>(p, line);
-    total = line.start[tiles];
-    if (tiles == 0) return;
-    const Cut cut = cut_of<kTileMinUnits>(total * kv.kv_heads, gridDim.x);
-    unit = cut.start(wg);
-    end = cut.start(wg + 1);
-    if (end > total * kv.kv_heads) end = total * kv.kv_heads;
-    if (unit >= end) return;
-    head = unit / total;
-    tile = part_of(line.start, tiles, unit - head * total);
-  } else {
-    head = wg / tiles_bound;
-    // later tiles see more keys: they start first
-    if (!direct_tile<R>(p, tiles_bound - 1 - wg % tiles_bound, lane, seq, tile_in_seq)) return;
-  }
-
-  while (unit < end) {
-    uint32_t b0 = 0;
-    if (split) {
-      if (tile == tiles) {
-        tile = 0;
-        ++head;
-      }
-      seq = part_of(line.first, kv.seqs, tile);
-      tile_in_seq = tile - line.first[seq];
-      b0 = unit - head * total - line.start[tile];
-    }
-    const Tile t = tile_info<R, B>(p, seq, tile_in_seq);
-    uint32_t b1 = units_of(t);
-    const uint32_t whole = b1;
-    if (split && b1 - b0 > end - unit) b1 = b0 + (end - unit);
-    const bool complete = b0 == 0 && b1 == whole;
+  Walk<R, B, kTileMinUnits> walk(p, line, split, tiles_bound, lane);
+  while (walk.next()) {
+    const Tile& t = walk.t;
+    const uint32_t b0 = walk.b0, b1 = walk.b1, head = walk.head, seq = walk.seq_index;
+    const bool complete = walk.complete;
 
     // ---- this lane's row ----
     const uint32_t r = wave * 32 + l32 < t.rows ? wave * 32 + l32 : t.rows - 1;
@@ -144,7 +111,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     // slot of key `lane` of block i
     auto slots = [&](uint32_t i) {
       const int32_t k = key0_of(i) + (int32_t)lane;
-      return i < nblk && k < t.hi ? slot_of(kv, t.seq, k) : -1;
+      return i < nblk && k < t.hi ? slot_of(kv, seq, k) : -1;
     };
     // The wave's share of the block's rows to LDS: load n covers rows (4 n + wave) RPW ..
     const uint32_t lrow = lane / CPR, lch = lane % CPR;
@@ -350,7 +317,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
                 u32x4{(uint32_t)x0[0], (uint32_t)x1[0], (uint32_t)x0[1], (uint32_t)x1[1]};
         }
     } else {
-      float* const part = partial_of<R, D>(p, 2 * wg + (b0 == 0));
+      float* const part = partial_of<R, D>(p, gridDim.x, 2 * walk.wg + (b0 == 0));
       if (mine) {
         float* const row = part + (size_t)r * D + 4 * h;
 #pragma unroll
@@ -365,9 +332,9 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         }
       }
     }
-    unit += split ? b1 - b0 : 1;
-    ++tile;
   }
+  walk.leave_note();
+  zero_unowned(p, blockIdx.x, gridDim.x);
 }
 
 }  // namespace

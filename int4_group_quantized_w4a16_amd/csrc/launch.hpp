@@ -238,7 +238,7 @@ struct PagedAttention {
 // sequence in the stream form, more in the tile form; other head_dims by rows.
 constexpr uint32_t kTileRows = 128, kTileKeys = 64, kTileMinUnits = 2;
 constexpr uint32_t kStreamRows = 16, kStreamKeys = 128, kStreamMinUnits = 1;
-constexpr uint32_t kSchedTiles = 1024;    // tiles (per K/V head) and sequences the split form's schedule holds
+constexpr uint32_t kSchedTiles = 512;     // tiles (per K/V head) and sequences the split form's schedule holds
 struct AttentionPlan {
   bool rows, stream, split;
   uint32_t tiles;           // bound on the tiles of one K/V head
@@ -259,7 +259,7 @@ constexpr AttentionPlan attention_plan(uint32_t kv_heads, uint32_t q_heads, uint
   const uint64_t slots = 2 * kComputeUnits;                 // workgroups resident at once
   a.split = tiles <= kSchedTiles && a.tiles * kv_heads < 4 * slots && (cap / keys + 2) * a.tiles * kv_heads < (1ull << 31);
   a.workgroups = (uint32_t)(a.split ? slots : a.tiles * kv_heads);
-  a.workspace = a.split ? slots * 2 * rows * (head_dim + 2) * 4 : 0;
+  a.workspace = a.split ? slots * (32 + 2 * rows * (head_dim + 2) * 4) : 0;
   return a;
 }
 hipError_t launch_attention_tile(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream);
