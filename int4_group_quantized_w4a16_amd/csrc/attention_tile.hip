@@ -191,16 +191,30 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 
       // does any of the wave's rows see any of the block's keys?
       if (!kEdge || (live && key0 <= wpos1)) {
+        // Left alone, the compiler reads each fragment just before its MFMA and waits out the LDS latency every
+        // time; the scheduling barriers keep the reads one group of MFMAs ahead.
         floatx16 s[2];
         const uint32_t kbase = l32 * L::kRow, kx = (h ^ kswz(l32)) * 16;
+        short8_t kf[2][4];
+        auto read_k = [&](int g) {       // k steps 2 g and 2 g + 1 of both score tiles
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+          for (int x = 0; x < 4; ++x)
+            kf[g & 1][x] = *reinterpret_cast<const short8_t*>(kb + (x & 1) * 32 * L::kRow +
+                                                              (kbase + (kx ^ ((2 * g + (x >> 1)) * 32))));
+        };
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[st][e] = 0.f;
+        read_k(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            s[st] = mfma32<kBf16>(
-                *reinterpret_cast<const short8_t*>(kb + st * 32 * L::kRow + (kbase + (kx ^ (k * 32)))), q[k], s[st]);
+        for (int g = 0; g < KS / 2; ++g) {
+          if (g + 1 < KS / 2) read_k(g + 1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[x & 1] = mfma32<kBf16>(kf[g & 1][x], q[2 * g + (x >> 1)], s[x & 1]);
+          __builtin_amdgcn_sched_barrier(0);
         }
         // element e of tile st is key 32 st + 8 (e / 4) + 4 h + e % 4
         if constexpr (kEdge) {
@@ -230,33 +244,43 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
           m = m1;
         }
         const float base = m == -INFINITY ? 0.f : -m;
-        short8_t w[4];     // weights: k step 2 st + (e >= 8), elements e % 8
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            u32x4 pk;
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float a = exp2_fast(__builtin_fmaf(s[st][8 * e2 + e], c, base));
-              const float b = exp2_fast(__builtin_fmaf(s[st][8 * e2 + e + 1], c, base));
-              l += a;
-              l += b;
-              pk[e / 2] = pack2<kBf16>(a, b);
-            }
-            w[2 * st + e2] = __builtin_bit_cast(short8_t, pk);
-          }
         // V^T fragment of k step ks, columns 32 d ..: keys 16 ks + 4 h + (0..3), and 8 further on
         const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
         const uint32_t vx = ((lane & 16) * 2 + (lane & 3) * 8) ^ (vswz(vrow) * 16);
-        auto vfrag = [&](int ks, int d) {
-          const char* const a = vb + ks * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
-          return join(read_tr(a), read_tr(a + 8 * L::kRow));
+        short8_t vf[2][DT];
+        auto read_v = [&](int ks) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const char* const a = vb + ks * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
+            vf[ks & 1][d] = join(read_tr(a), read_tr(a + 8 * L::kRow));
+          }
         };
+        short8_t w[4];
+        auto weigh = [&](int ks) {       // weights of k step ks: elements 8 (ks % 2) .. + 7 of tile ks / 2
+          u32x4 pk;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+          for (int e = 0; e < 8; e += 2) {
+            const float a = exp2_fast(__builtin_fmaf(s[ks >> 1][8 * (ks & 1) + e], c, base));
+            const float b = exp2_fast(__builtin_fmaf(s[ks >> 1][8 * (ks & 1) + e + 1], c, base));
+            l += a;
+            l += b;
+            pk[e / 2] = pack2<kBf16>(a, b);
+          }
+          w[ks] = __builtin_bit_cast(short8_t, pk);
+        };
+        // each step's weights are made under the previous step's MFMAs
+        read_v(0);
+        weigh(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vfrag(ks, d), w[ks], o[d]);
+        for (int ks = 0; ks < 4; ++ks) {
+          if (ks < 3) read_v(ks + 1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[ks & 1][d], w[ks], o[d]);
+          if (ks < 3) weigh(ks + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
         if constexpr (kEdge) {
           if (special) {
             // the non-finite values of the block, from the cache, to the rows that see their key
