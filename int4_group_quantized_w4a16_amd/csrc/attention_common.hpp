@@ -37,6 +37,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// The two 16-bit values of pack2 added to acc (f32, subnormals kept).
+template <bool kBf16>
+__device__ __forceinline__ float add2(uint32_t pair, float acc) {
+  if constexpr (kBf16) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, pair), v2{(__bf16)1.0f, (__bf16)1.0f}, acc, false);
+  } else {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, pair), half2_t{(_Float16)1.0f, (_Float16)1.0f}, acc, false);
+  }
+}
+
 // Transposed read of four rows (keys) x 16 columns of 16-bit values per group
 // of 16 lanes: lane i of the group points at 8 bytes, columns 4 (i % 4) .. + 3
 // of row i / 4, and receives column i of the four rows.
@@ -106,17 +117,58 @@ __device__ __forceinline__ float with_special(float x, float nan, float pos, flo
   return nan > 0.f ? NAN : x;
 }
 
-// Direct global -> LDS load of 16 bytes per lane: from base + off (base
-// wave-uniform) to lds + 16 * lane.  The buffer form, whose pending loads the
-// compiler does not hold against LDS reads; callers wait by wait_vm_barrier.
-__device__ __forceinline__ void dma16(const char* base, uint32_t off, char* lds) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+__device__ __forceinline__ u32x4 raw_rsrc(const char* base) {   // raw buffer, no range limit
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32), 0xFFFFFFFFu, 0x00020000u};
 }
-// Waits until at most N vector-memory operations of the wave are outstanding, then meets the others.
+// Direct global -> LDS load of 16 bytes per lane: from base + off (base
+// wave-uniform) to lds + 16 * lane.  In assembly (no register is written): from
+// the builtin the compiler knows that LDS changes, cannot tell the buffers of a
+// ring apart, and waits for every load in flight before a read of any.  Callers
+// wait by wait_vm_barrier; the compiler's own counts for other loads only get
+// stricter by loads that it does not see.  The wait states cover m0 and a
+// descriptor that a lane read has just written.
+template <int kBytes>
+__device__ __forceinline__ void dma(const char* base, uint32_t off, void* lds) {
+  const u32x4 rsrc = raw_rsrc(base);
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  if constexpr (kBytes == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rsrc) : "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rsrc) : "m0");
+}
+// A K and a V load of the same cache rows: from the descriptors' bases + slot *
+// row_bytes (32 bits) + the lane's offsets to lds and lds + kApart.
+template <int kApart>
+__device__ __forceinline__ void dma16_pair(u32x4 krsrc, uint32_t koff, u32x4 vrsrc, uint32_t voff, uint32_t slot,
+                                           uint32_t row_bytes, void* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  uint32_t row;
+  asm volatile("s_mul_i32 %0, %1, %2\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %6, %0 offen lds\n\t"
+               "s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %8, %0 offen lds"
+               : "=&s"(row)
+               : "s"(slot), "s"(row_bytes), "s"(at), "n"(kApart), "v"(koff), "s"(krsrc), "v"(voff), "s"(vrsrc)
+               : "m0", "scc");
+}
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, void* lds) { dma<16>(base, off, lds); }
+__device__ __forceinline__ void dma4(const char* base, uint32_t off, void* lds) { dma<4>(base, off, lds); }
+// Waits until at most N vector-memory operations of the wave are outstanding,
+// and its LDS operations are done.  By the builtin (vmcnt in bits 0-3 and
+// 14-15, expcnt 4-6, lgkmcnt 8-11): the compiler then knows that older loads
+// have landed and adds no waits of its own for them.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// ... and meets the other waves.
 template <int N>
 __device__ __forceinline__ void wait_vm_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  wait_vm<N>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ short8_t join(short4_t a, short4_t b) {

@@ -71,7 +71,7 @@ __device__ __forceinline__ Tile tile_info(const PagedAttention& p, const Seq& q,
   t.p1 = q.a + (int32_t)p.group.div(t.row0 + t.rows - 1) + t.shift;
   t.hi = t.p1 < (int32_t)p.kv.cap ? t.p1 + 1 : (int32_t)p.kv.cap;
   t.ns = t.wb0 = t.count = 0;
-  if (t.hi <= 0) {
+  if (t.hi <= 0 || p.kv.pages == 0) {
     t.hi = 0;
     return t;
   }

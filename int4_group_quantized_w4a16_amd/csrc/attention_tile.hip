@@ -5,19 +5,24 @@
 // * Workgroup = 4 waves, 128 packed rows (token * group + head) of one
 //   (sequence, K/V head); wave w owns rows 32w .. 32w+31 and keeps their Q
 //   fragments, running maximum, sum and output in registers.  Keys pass in
-//   blocks of 64 through two LDS buffers shared by the waves (33 KiB each at
-//   128 columns), so two workgroups share a CU and one's softmax runs under
-//   the other's matrix instructions.
+//   tiles of 32 (blocks of two) through a ring of four LDS buffers shared by
+//   the waves (16 KiB each at 128 columns), so two workgroups share a CU.
+// * Software pipeline: while the vector unit turns tile t's scores into
+//   weights, the matrix unit makes tile t+1's scores; while it then multiplies
+//   tile t's weights with V, the vector unit finds tile t+1's maxima.  The
+//   exponentials (16 cycles each for 64 lanes) take about as long as the
+//   MFMAs, so neither can wait for the other: one 64-key block at a time
+//   without this overlap ran 8192 causal keys, 32 heads of 128 columns, in
+//   764 us.
 // * Scores are computed transposed, S^T = K.Q^T (32x32x16 MFMA, K the A
 //   operand): a lane then holds, for ITS row, 16 keys of each 32, and their
 //   weights in exactly the order in which it feeds them to the second product
 //   O^T = V^T.P^T as B operand, with k index (h, j) standing for key
 //   8 (j / 4) + 4 h + j % 4 of 16.  Weights never leave the lane; V^T comes
 //   from transposed LDS reads of four keys each in the same order.
-// * The cache rows of the next block go straight to LDS (direct loads) while
-//   the current one is computed on; one barrier per block.  Lane j of each
-//   wave looks up the slot of key j one block ahead of that.  A load covers 4
-//   (64 columns: 8) keys; where they share a page (page_size a multiple of
+// * The cache rows of a tile go straight to LDS (direct loads) three tiles
+//   ahead; one barrier per tile.  Lane j of each wave looks up the slot of key
+//   j of a block, a block ahead of that.  A load covers 4 (64 columns: 8) keys; where they share a page (page_size a multiple of
 //   that) it takes a wave-uniform 64-bit base and one lane offset, otherwise
 //   one load per key.
 // * LDS rows are unpadded (a direct load writes lane-contiguous chunks), so
@@ -42,14 +47,17 @@ namespace kaio {
 namespace {
 
 constexpr uint32_t R = kTileRows, B = kTileKeys;
-static_assert(R == 128 && B == 64, "four waves of 32 rows, blocks of two 32-key score tiles");
+static_assert(R == 128 && B == 64, "four waves of 32 rows, blocks of two 32-key tiles");
 
 template <int D>
 struct Lds {
   static constexpr int kRow = D * 2;         // bytes
-  static constexpr int kV = B * kRow;        // offset of V in a buffer
+  static constexpr int kV = 32 * kRow;       // offset of V in a tile's buffer
   static constexpr int kSize = 2 * kV;
 };
+
+// by value: a choice between variables would keep them, and what is captured with them, in memory
+__device__ __forceinline__ int32_t pick(uint32_t i, int32_t a, int32_t b, int32_t c) { return i == 0 ? a : i == 1 ? b : c; }
 
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p, bool split, uint32_t tiles_bound) {
@@ -58,9 +66,17 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
   constexpr int DT = D / 32;            // 32-column tiles of the output
   constexpr int CPR = D / 8;            // 16-byte chunks per row
   constexpr int RPW = 64 / CPR;         // rows per direct load of a wave
-  constexpr int NL = B / RPW / 4;       // direct loads per wave, block and tensor
-  __shared__ __attribute__((aligned(256))) char buf[2][L::kSize];
-  __shared__ uint32_t flags[2][4];      // per buffer and wave: V holds non-finite values
+  constexpr int NL = 32 / RPW / 4;      // direct loads per wave, tile and tensor
+  // one object: reads of one that direct loads write do not wait for direct loads to another
+  struct Shared {
+    char ring[4][L::kSize];
+    uint32_t ids[4][4][64];             // per wave: page ids of four blocks' keys
+    uint32_t flags[4];                  // per wave: V of the tile holds non-finite values
+  };
+  __shared__ __attribute__((aligned(256))) Shared sh;
+  auto& ring = sh.ring;
+  auto& ids = sh.ids;
+  auto& flags = sh.flags;
   extern __shared__ char dyn[];
   Line& line = *reinterpret_cast<Line*>(dyn);   // split form only
 
@@ -68,10 +84,15 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
   const uint32_t tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t g = p.group.d;
-  const size_t row_elems = (size_t)kv.kv_heads * D;       // a cache slot
+  const size_t row_bytes = (size_t)kv.kv_heads * D * 2;   // a cache slot
+  // Keys that a load covers share a page: one slot, a scalar offset, serves RPW keys, where the offsets of the cache
+  // fit in 32 bits.  Otherwise a load per key.
+  const bool grouped = kv.page.d % RPW == 0 && (uint64_t)kv.pages * kv.page.d * row_bytes <= 0xFFFFFFFFull;
+  constexpr uint32_t kGroupShift = D == 128 ? 2 : 3;
+  static_assert((1 << kGroupShift) == RPW, "keys per load");
+  const uint32_t ks = grouped ? kGroupShift : 0;          // keys per slot looked up: 1 << ks
   const bool negate = p.scale < 0.f;
   const float c = fmaxf(fabsf(p.scale) * 1.44269504088896341f, 1.17549435e-38f);
-
   Walk<R, B, kTileMinUnits> walk(p, line, split, tiles_bound, lane);
   while (walk.next()) {
     const Tile& t = walk.t;
@@ -85,9 +106,6 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     const int32_t pos = t.q0 + (int32_t)tok + t.shift;
     const int32_t floor = window_floor(p, pos);
     const int32_t sinks = p.window ? (int32_t)(p.sinks < 0x7FFFFFFFu ? p.sinks : 0x7FFFFFFFu) : 0;
-    // rows are in order of their positions: the wave's first and last
-    const int32_t wpos0 = __builtin_amdgcn_readlane(pos, 0), wpos1 = __builtin_amdgcn_readlane(pos, 31);
-    const int32_t wfloor1 = __builtin_amdgcn_readlane(floor, 31);
     const int32_t tfloor1 = window_floor(p, t.p1);
 
     short8_t q[KS];
@@ -108,46 +126,73 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       const uint32_t b = b0 + i;
       return (int32_t)((b < t.ns ? b : t.wb0 + (b - t.ns)) * B);
     };
-    // slot of key `lane` of block i
-    auto slots = [&](uint32_t i) {
-      const int32_t k = key0_of(i) + (int32_t)lane;
-      return i < nblk && k < t.hi ? slot_of(kv, seq, k) : -1;
+    // Slots, one per 1 << ks keys: window w is blocks w << ks .., lane j its j-th group of keys.  In two steps: the
+    // page ids go to LDS by a direct load (a register load here would make the compiler wait for everything in
+    // flight where it is used), and are read a window later.
+    const char* const table = reinterpret_cast<const char*>(kv.table + (size_t)seq * kv.width);
+    auto group_key = [&](uint32_t w) {              // first key of this lane's group; its block
+      const uint32_t blk = (w << ks) + (lane >> (6 - ks));
+      return (uint32_t)key0_of(blk) + ((lane & ((64u >> ks) - 1)) << ks);
     };
-    // The wave's share of the block's rows to LDS: load n covers rows (4 n + wave) RPW ..
+    auto request = [&](uint32_t w) {                // returns the group's place in its page
+      const uint32_t k = group_key(w), kc = k < kv.cap ? k : kv.cap - 1, pg = kv.page.div(kc);
+      dma4(table, pg * 4, ids[wave][w & 3]);
+      return kc - pg * kv.page.d;
+    };
+    auto slots = [&](uint32_t w, uint32_t place) {
+      const uint32_t id = ids[wave][w & 3][lane];
+      return (w << ks) + (lane >> (6 - ks)) < nblk && (int32_t)group_key(w) < t.hi && id < kv.pages
+                 ? (int32_t)(id * kv.page.d + place) : -1;
+    };
+    // lane of slots() that has key j of block i (j a multiple of 1 << ks, or anything in its group)
+    auto slot_lane = [&](uint32_t i, uint32_t j) { return ((i & ((1u << ks) - 1)) << (6 - ks)) + (j >> ks); };
+    // The wave's share of a tile's rows to ring buffer b: load n covers rows (4 n + wave) RPW .. of keys 32 half ..
+    // of block i, whose slots these are.  Always the same number of loads (the waits count them): absent slots read
+    // slot 0, which is there.
     const uint32_t lrow = lane / CPR, lch = lane % CPR;
-    const bool shared_page = kv.page.d % RPW == 0;
     auto kswz = [](uint32_t row) { return D == 128 ? (row & 15) : ((row >> 1) & 7); };            // of a 16-byte chunk
     auto vswz = [](uint32_t row) { return (D == 128 ? (row & 3) : ((row >> 1) & 1)) * 4; };
-    auto fetch = [&](uint32_t buffer, int32_t slot) {
+    const char* const khead = reinterpret_cast<const char*>(kv.k) + (size_t)head * D * 2;
+    const char* const vhead = reinterpret_cast<const char*>(kv.v) + (size_t)head * D * 2;
+    const u32x4 krsrc = raw_rsrc(khead), vrsrc = raw_rsrc(vhead);
+    uint32_t koff[NL], voff[NL];
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const uint32_t row = (4 * n + wave) * RPW + lrow, off = grouped ? lrow * (uint32_t)row_bytes : 0;
+      koff[n] = off + (lch ^ kswz(row)) * 16;
+      voff[n] = off + (lch ^ vswz(row)) * 16;
+    }
+    auto fetch = [&](uint32_t b, int32_t slot, uint32_t i, int half) {
+      const int32_t there = slot < 0 ? 0 : slot;
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
-        const uint32_t row0 = (4 * n + wave) * RPW, row = row0 + lrow;
-        char* const kl = buf[buffer] + row0 * L::kRow;
-        const uint32_t koff = (lch ^ kswz(row)) * 16, voff = (lch ^ vswz(row)) * 16;
-        if (shared_page) {
-          // keys past t.hi or of an absent page share their first key's fate or lie in its page: valid memory
-          const int32_t s0 = __builtin_amdgcn_readlane(slot, (int)row0);
-          const size_t at = ((size_t)(s0 < 0 ? 0 : s0) * row_elems + head * D) * 2;
-          const uint32_t lane_off = lrow * (uint32_t)(row_elems * 2);
-          dma16(reinterpret_cast<const char*>(kv.k) + at, lane_off + koff, kl);
-          dma16(reinterpret_cast<const char*>(kv.v) + at, lane_off + voff, kl + L::kV);
+        const uint32_t row0 = (4 * n + wave) * RPW;
+        char* const kl = ring[b] + row0 * L::kRow;
+        if (grouped) {
+          const uint32_t s0 = __builtin_amdgcn_readlane(there, (int)slot_lane(i, half * 32 + row0));
+          dma16_pair<L::kV>(krsrc, koff[n], vrsrc, voff[n], s0, (uint32_t)row_bytes, kl);
         } else {
 #pragma unroll 1
           for (uint32_t j = 0; j < (uint32_t)RPW; ++j) {
-            const int32_t s0 = __builtin_amdgcn_readlane(slot, (int)(row0 + j));
-            const size_t at = ((size_t)(s0 < 0 ? 0 : s0) * row_elems + head * D) * 2;
+            const uint32_t s0 = __builtin_amdgcn_readlane(there, (int)(half * 32 + row0 + j));
+            const size_t at = (size_t)s0 * row_bytes;
             if (lrow == j) {
-              dma16(reinterpret_cast<const char*>(kv.k) + at, koff, kl);
-              dma16(reinterpret_cast<const char*>(kv.v) + at, voff, kl + L::kV);
+              dma16(khead + at, koff[n], kl);
+              dma16(vhead + at, voff[n], kl + L::kV);
             }
           }
         }
       }
     };
-    // zeroes V of absent slots and non-finite values; notes whether there are any of the latter
-    auto fix_v = [&](uint32_t buffer, uint64_t live) {
+    // all but the newest tile's loads of the wave have landed; everybody is here
+    auto wait_tile = [&] {
+      if (grouped) wait_vm_barrier<2 * NL>();
+      else wait_vm_barrier<2 * NL * RPW>();
+    };
+    // zeroes V of absent slots and non-finite values of the tile in buffer b; are there any of the latter?
+    auto fix_v = [&](uint32_t b, uint32_t live) {
       bool special = false;
-      char* const vl = buf[buffer] + L::kV;
+      char* const vl = ring[b] + L::kV;
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const uint32_t at = (n * 256 + tid) * 16, row = at / L::kRow;
@@ -163,162 +208,204 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         }
         if (change) *reinterpret_cast<u32x4*>(vl + at) = v;
       }
-      flags[buffer][wave] = __ballot(special) != 0;
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      return (flags[buffer][0] | flags[buffer][1] | flags[buffer][2] | flags[buffer][3]) != 0;
+      flags[wave] = __ballot(special) != 0;
+      wait_vm_barrier<63>();   // LDS only
+      return (flags[0] | flags[1] | flags[2] | flags[3]) != 0;
     };
     // some row of the tile does not see some key of the block that starts at key0
     auto edge_of = [&](int32_t key0) {
       return key0 + (int32_t)B - 1 > t.p0 || (p.window && key0 <= tfloor1 && key0 + (int32_t)B > sinks);
     };
 
-    int32_t slot = slots(0), slot_next = slots(1);
-    uint64_t live = __ballot(slot >= 0);
-    if (live) fetch(0, slot);
-    wait_vm_barrier<0>();
+    // K fragments of tile buffer b: k steps 4 j .. 4 j + 3
+    const uint32_t kbase = l32 * L::kRow, kx = (h ^ kswz(l32)) * 16;
+    short8_t kf[2][4];
+    auto read_k = [&](uint32_t b, int j) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        kf[j][x] = *reinterpret_cast<const short8_t*>(ring[b] + (kbase + (kx ^ ((4 * j + x) * 32))));
+    };
+    // V^T fragments of a k step (16 keys), columns 32 d ..: its keys 4 h + (0..3), and 8 further on
+    const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
+    const uint32_t vx = ((lane & 16) * 2 + (lane & 3) * 8) ^ (vswz(vrow) * 16);
+    short8_t vf[2][DT];
+    auto read_v = [&](uint32_t b, int step_k) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const char* const a = ring[b] + L::kV + step_k * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
+        vf[step_k][d] = join(read_tr(a), read_tr(a + 8 * L::kRow));
+      }
+    };
+    floatx16 s[2];                       // scores: element e is key 8 (e / 4) + 4 h + e % 4 of the tile
+    auto scores = [&](floatx16& sc, int j) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc = mfma32<kBf16>(kf[j][x], q[4 * j + x], sc);
+    };
+    auto max_of = [&](const floatx16& sc) {
+      float top = sc[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, sc[e]);
+      return max_halves(top) * c;
+    };
 
-    // One block.  kEdge: some row does not see some key (of the tile's rows: the choice is the workgroup's).
-    auto block = [&](auto edge_tag, uint32_t i) {
+    int32_t sl0 = -1, sl1 = -1, sl2 = -1;    // slots of this window's keys and of the next two's
+    uint32_t place = 0;                      // of window w + 2 at the start of window w
+    float top = 0.f;
+    if (nblk) {
+      const uint32_t p0 = request(0), p1 = request(1);
+      place = request(2);
+      wait_vm<0>();   // the ids are the wave's own
+      sl0 = slots(0, p0);
+      sl1 = slots(1, p1);
+      fetch(0, sl0, 0, 0);
+      fetch(1, sl0, 0, 1);
+      fetch(2, pick(!grouped, sl0, sl1, sl1), 1, 0);
+      if (grouped) wait_vm_barrier<4 * NL>();
+      else wait_vm_barrier<4 * NL * RPW>();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[0][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KS / 4; ++j) {
+        read_k(0, j);
+        scores(s[0], j);
+      }
+      top = max_of(s[0]);
+    }
+
+    // Tile 2 i + half of the piece; its scores and their maxima are there.  kEdge: some row does not see some key
+    // of the block (of the tile's rows: the choice is the workgroup's).
+    auto step = [&](auto edge_tag, auto half_tag, uint32_t i) {
       constexpr bool kEdge = decltype(edge_tag)::value;
-      const int32_t key0 = key0_of(i);
-      const char* const kb = buf[i & 1];
-      const char* const vb = kb + L::kV;
-      const uint64_t live_next = __ballot(slot_next >= 0);
-      if (live_next) fetch((i + 1) & 1, slot_next);
-      const int32_t slot_after = slots(i + 2);
+      constexpr int kHalf = decltype(half_tag)::value;
+      const uint32_t b = 2 * (i & 1) + kHalf, bn = (b + 1) & 3;
+      floatx16& sc = s[kHalf];
+      floatx16& sn = s[1 - kHalf];
+      wait_tile();                       // the next tile is in place, the one before this no longer read
+      if (kHalf == 0 && (i & ((1u << ks) - 1)) == 0) {
+        sl2 = slots((i >> ks) + 2, place);
+        place = request((i >> ks) + 3);
+      }
+      const uint32_t in = i + 1 + kHalf, wn = (in >> ks) - (i >> ks);   // of the tile three on
+      fetch((b + 3) & 3, pick(wn, sl0, sl1, sl2), in, 1 - kHalf);
+      read_k(bn, 0);
       bool special = false;
-      if constexpr (kEdge) special = fix_v(i & 1, live);
-
-      // does any of the wave's rows see any of the block's keys?
-      if (!kEdge || (live && key0 <= wpos1)) {
-        // Left alone, the compiler reads each fragment just before its MFMA and waits out the LDS latency every
-        // time; the scheduling barriers keep the reads one group of MFMAs ahead.
-        floatx16 s[2];
-        const uint32_t kbase = l32 * L::kRow, kx = (h ^ kswz(l32)) * 16;
-        short8_t kf[2][4];
-        auto read_k = [&](int g) {       // k steps 2 g and 2 g + 1 of both score tiles
+      uint32_t there = 0;
+      if constexpr (kEdge) {
+        const int32_t tile0 = key0_of(i) + 32 * kHalf;
+        const int32_t mine = __shfl(sl0, (int)slot_lane(i, 32 * kHalf + l32));
+        there = (uint32_t)__ballot(mine >= 0 && tile0 + (int32_t)l32 < t.hi);
+        special = fix_v(b, there);
+        const uint32_t bits = there >> (4 * h);
+        const int32_t key0 = tile0 + 4 * (int32_t)h;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            kf[g & 1][x] = *reinterpret_cast<const short8_t*>(kb + (x & 1) * 32 * L::kRow +
-                                                              (kbase + (kx ^ ((2 * g + (x >> 1)) * 32))));
-        };
+        for (int e = 0; e < 16; ++e) {
+          const int off = 8 * (e / 4) + e % 4;
+          const int32_t key = key0 + off;
+          const bool sees = key <= pos && (key > floor || key < sinks) && ((bits >> off) & 1);
+          sc[e] = sees ? sc[e] : -INFINITY;
+        }
+        top = max_of(sc);
+      }
+      if (__any(top > m + kLag)) {
+        const float m1 = fmaxf(m, top);
+        const float old = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
+        l *= old;
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[st][e] = 0.f;
-        read_k(0);
+          for (int e = 0; e < 16; ++e) o[d][e] *= old;
+        m = m1;
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      short8_t w[2];
+      auto weigh = [&](int step_k) {     // weights of a k step
+        u32x4 pk;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float a = exp2_fast(__builtin_fmaf(sc[8 * step_k + e], c, base));
+          const float b = exp2_fast(__builtin_fmaf(sc[8 * step_k + e + 1], c, base));
+          pk[e / 2] = pack2<kBf16>(a, b);
+          l = add2<kBf16>(pk[e / 2], l);
+        }
+        w[step_k] = __builtin_bit_cast(short8_t, pk);
+      };
+      // Left alone, the compiler reads each fragment just before its MFMA and waits out the LDS latency every
+      // time; the scheduling barriers keep the reads one group of MFMAs ahead.
+      if constexpr (KS > 4) read_k(bn, 1);
+      else read_v(b, 0);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sn[e] = 0.f;
+      __builtin_amdgcn_sched_barrier(0);
+      scores(sn, 0);
+      weigh(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (KS > 4) {
+        read_v(b, 0);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int g = 0; g < KS / 2; ++g) {
-          if (g + 1 < KS / 2) read_k(g + 1);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[x & 1] = mfma32<kBf16>(kf[g & 1][x], q[2 * g + (x >> 1)], s[x & 1]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        // element e of tile st is key 32 st + 8 (e / 4) + 4 h + e % 4
-        if constexpr (kEdge) {
-          const uint32_t lo32 = (uint32_t)(live >> (4 * h)), hi32 = (uint32_t)(live >> (32 + 4 * h));
-#pragma unroll
-          for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int off = 8 * (e / 4) + e % 4;
-              const int32_t key = key0 + 32 * st + off + 4 * (int32_t)h;
-              const bool sees = key <= pos && (key > floor || key < sinks) && (((st ? hi32 : lo32) >> off) & 1);
-              s[st][e] = sees ? s[st][e] : -INFINITY;
-            }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int e = 1; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-        top = max_halves(top) * c;
-        if (__any(top > m + kLag)) {
-          const float m1 = fmaxf(m, top);
-          const float old = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
-          l *= old;
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[d][e] *= old;
-          m = m1;
-        }
-        const float base = m == -INFINITY ? 0.f : -m;
-        // V^T fragment of k step ks, columns 32 d ..: keys 16 ks + 4 h + (0..3), and 8 further on
-        const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
-        const uint32_t vx = ((lane & 16) * 2 + (lane & 3) * 8) ^ (vswz(vrow) * 16);
-        short8_t vf[2][DT];
-        auto read_v = [&](int ks) {
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const char* const a = vb + ks * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
-            vf[ks & 1][d] = join(read_tr(a), read_tr(a + 8 * L::kRow));
-          }
-        };
-        short8_t w[4];
-        auto weigh = [&](int ks) {       // weights of k step ks: elements 8 (ks % 2) .. + 7 of tile ks / 2
-          u32x4 pk;
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float a = exp2_fast(__builtin_fmaf(s[ks >> 1][8 * (ks & 1) + e], c, base));
-            const float b = exp2_fast(__builtin_fmaf(s[ks >> 1][8 * (ks & 1) + e + 1], c, base));
-            l += a;
-            l += b;
-            pk[e / 2] = pack2<kBf16>(a, b);
-          }
-          w[ks] = __builtin_bit_cast(short8_t, pk);
-        };
-        // each step's weights are made under the previous step's MFMAs
-        read_v(0);
-        weigh(0);
+        scores(sn, 1);
+        weigh(1);
         __builtin_amdgcn_sched_barrier(0);
+      }
+      read_v(b, 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks < 3) read_v(ks + 1);
-          __builtin_amdgcn_sched_barrier(0);
+      for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[0][d], w[0], o[d]);
+      if constexpr (KS <= 4) weigh(1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[ks & 1][d], w[ks], o[d]);
-          if (ks < 3) weigh(ks + 1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (kEdge) {
-          if (special) {
-            // the non-finite values of the block, from the cache, to the rows that see their key
-            typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
-            const u32x16 wv = __builtin_bit_cast(u32x16, w);
+      for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[1][d], w[1], o[d]);
+      top = max_of(sn);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (kEdge) {
+        if (special) {
+          // the non-finite values of the tile, from the cache, to the rows that see their key
+          typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+          const u32x8 wv = __builtin_bit_cast(u32x8, w);
 #pragma unroll 1
-            for (int j = 0; j < (int)B; ++j) {      // key j: an element of half (j / 4) % 2
-              const int32_t sj = __builtin_amdgcn_readlane(slot, j);
-              const int in32 = j & 31, half = (in32 >> 2) & 1, e = 4 * (in32 >> 3) + (in32 & 3);
-              const uint32_t pair = wv[8 * (j >> 5) + (e >> 1)];
-              const uint32_t pw = __shfl(e & 1 ? pair >> 16 : pair & 0xFFFFu, (int)l32 + 32 * half);
-              const float x = to_f32<kBf16>((uint16_t)pw);
-              if (sj < 0) continue;
-              const uint16_t* const row = kv.v + (size_t)sj * row_elems + head * D + 4 * h;
+          for (int j = 0; j < 32; ++j) {            // key j: an element of half (j / 4) % 2
+            const int32_t s0 = __builtin_amdgcn_readlane(sl0, (int)slot_lane(i, 32 * kHalf + j));
+            const int32_t sj = (there >> j) & 1 ? s0 + (j & ((1 << ks) - 1)) : -1;
+            const int in_half = (j >> 2) & 1, e = 4 * (j >> 3) + (j & 3);
+            const uint32_t pair = wv[e >> 1];
+            const uint32_t pw = __shfl(e & 1 ? pair >> 16 : pair & 0xFFFFu, (int)l32 + 32 * in_half);
+            const float x = to_f32<kBf16>((uint16_t)pw);
+            if (sj < 0) continue;
+            const uint16_t* const row = reinterpret_cast<const uint16_t*>(vhead + (size_t)sj * row_bytes) + 4 * h;
 #pragma unroll
-              for (int d = 0; d < DT; ++d)
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const u32x2 v = *reinterpret_cast<const u32x2*>(row + d * 32 + k * 8);
+              for (int k = 0; k < 4; ++k) {
+                const u32x2 v = *reinterpret_cast<const u32x2*>(row + d * 32 + k * 8);
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    const float vf = to_f32<kBf16>((uint16_t)(v[y >> 1] >> (16 * (y & 1))));
-                    o[d][4 * k + y] += x != 0.f && !(fabsf(vf) < INFINITY) ? x * vf : 0.f;
-                  }
+                for (int y = 0; y < 4; ++y) {
+                  const float vv = to_f32<kBf16>((uint16_t)(v[y >> 1] >> (16 * (y & 1))));
+                  o[d][4 * k + y] += x != 0.f && !(fabsf(vv) < INFINITY) ? x * vv : 0.f;
                 }
-            }
+              }
           }
+          wait_vm<0>();   // or the compiler waits for these loads in the common loop
         }
       }
-      slot = slot_next;
-      slot_next = slot_after;
-      live = live_next;
-      wait_vm_barrier<0>();   // the next block is in place, this one no longer read
+    };
+    auto block = [&](auto edge_tag, uint32_t i) {
+      step(edge_tag, std::integral_constant<int, 0>{}, i);
+      step(edge_tag, std::integral_constant<int, 1>{}, i);
+      if (((i + 1) & ((1u << ks) - 1)) == 0) {
+        sl0 = sl1;
+        sl1 = sl2;
+      }
+    };
+    // every row sees every key of block i, and all are there
+    const uint32_t group_bits = 64u >> ks;
+    auto clean = [&](uint32_t i) {
+      const uint64_t absent = __ballot(sl0 < 0) >> ((i & ((1u << ks) - 1)) * group_bits);
+      return !edge_of(key0_of(i)) && (absent << (64 - group_bits)) == 0;
     };
     for (uint32_t i = 0; i < nblk;) {
-      for (; i < nblk && (edge_of(key0_of(i)) || ~live); ++i) block(std::true_type{}, i);
-      for (; i < nblk && !(edge_of(key0_of(i)) || ~live); ++i) block(std::false_type{}, i);
+      for (; i < nblk && !clean(i); ++i) block(std::true_type{}, i);
+      for (; i < nblk && clean(i); ++i) block(std::false_type{}, i);
     }
+    wait_vm_barrier<0>();   // the loads past the end have landed before the ring is used again
 
     // ---- the piece's result ----
     l = add_halves(l);
