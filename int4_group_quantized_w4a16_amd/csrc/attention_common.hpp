@@ -163,7 +163,12 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
   asm volatile("" ::: "memory");
 }
-// ... and meets the other waves.
+// At most N LDS operations outstanding (vector memory aside).
+template <int N>
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (N << 8) | (3 << 14));
+}
+// wait_vm, and meets the other waves.
 template <int N>
 __device__ __forceinline__ void wait_vm_barrier() {
   wait_vm<N>();

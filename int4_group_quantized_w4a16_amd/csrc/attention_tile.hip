@@ -59,7 +59,9 @@ struct Lds {
 // by value: a choice between variables would keep them, and what is captured with them, in memory
 __device__ __forceinline__ int32_t pick(uint32_t i, int32_t a, int32_t b, int32_t c) { return i == 0 ? a : i == 1 ? b : c; }
 
-template <bool kBf16, int D>
+// kGrouped: keys that a load covers share a page, so one slot, a scalar offset, serves them all (and the offsets of
+// the cache fit in 32 bits).  Otherwise a load per key.
+template <bool kBf16, int D, bool kGrouped>
 __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p, bool split, uint32_t tiles_bound) {
   using L = Lds<D>;
   constexpr int KS = D / 16;            // k steps of the first product
@@ -85,14 +87,13 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t g = p.group.d;
   const size_t row_bytes = (size_t)kv.kv_heads * D * 2;   // a cache slot
-  // Keys that a load covers share a page: one slot, a scalar offset, serves RPW keys, where the offsets of the cache
-  // fit in 32 bits.  Otherwise a load per key.
-  const bool grouped = kv.page.d % RPW == 0 && (uint64_t)kv.pages * kv.page.d * row_bytes <= 0xFFFFFFFFull;
-  constexpr uint32_t kGroupShift = D == 128 ? 2 : 3;
-  static_assert((1 << kGroupShift) == RPW, "keys per load");
-  const uint32_t ks = grouped ? kGroupShift : 0;          // keys per slot looked up: 1 << ks
   const bool negate = p.scale < 0.f;
   const float c = fmaxf(fabsf(p.scale) * 1.44269504088896341f, 1.17549435e-38f);
+  constexpr uint32_t ks = !kGrouped ? 0 : D == 128 ? 2 : 3;   // keys per slot looked up: 1 << ks
+  constexpr uint32_t kPer = 1u << ks;                         // blocks per window of 64 slots
+  static_assert(!kGrouped || kPer == RPW, "keys per load");
+  constexpr int kLoads = 2 * NL * (kGrouped ? 1 : RPW);       // of a wave per tile
+
   Walk<R, B, kTileMinUnits> walk(p, line, split, tiles_bound, lane);
   while (walk.next()) {
     const Tile& t = walk.t;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
                  ? (int32_t)(id * kv.page.d + place) : -1;
     };
     // lane of slots() that has key j of block i (j a multiple of 1 << ks, or anything in its group)
-    auto slot_lane = [&](uint32_t i, uint32_t j) { return ((i & ((1u << ks) - 1)) << (6 - ks)) + (j >> ks); };
+    auto slot_lane = [&](uint32_t i, uint32_t j) { return ((i % kPer) << (6 - ks)) + (j >> ks); };
     // The wave's share of a tile's rows to ring buffer b: load n covers rows (4 n + wave) RPW .. of keys 32 half ..
     // of block i, whose slots these are.  Always the same number of loads (the waits count them): absent slots read
     // slot 0, which is there.
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     uint32_t koff[NL], voff[NL];
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-      const uint32_t row = (4 * n + wave) * RPW + lrow, off = grouped ? lrow * (uint32_t)row_bytes : 0;
+      const uint32_t row = (4 * n + wave) * RPW + lrow, off = kGrouped ? lrow * (uint32_t)row_bytes : 0;
       koff[n] = off + (lch ^ kswz(row)) * 16;
       voff[n] = off + (lch ^ vswz(row)) * 16;
     }
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       for (int n = 0; n < NL; ++n) {
         const uint32_t row0 = (4 * n + wave) * RPW;
         char* const kl = ring[b] + row0 * L::kRow;
-        if (grouped) {
+        if constexpr (kGrouped) {
           const uint32_t s0 = __builtin_amdgcn_readlane(there, (int)slot_lane(i, half * 32 + row0));
           dma16_pair<L::kV>(krsrc, koff[n], vrsrc, voff[n], s0, (uint32_t)row_bytes, kl);
         } else {
@@ -183,11 +184,6 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
           }
         }
       }
-    };
-    // all but the newest tile's loads of the wave have landed; everybody is here
-    auto wait_tile = [&] {
-      if (grouped) wait_vm_barrier<2 * NL>();
-      else wait_vm_barrier<2 * NL * RPW>();
     };
     // zeroes V of absent slots and non-finite values of the tile in buffer b; are there any of the latter?
     auto fix_v = [&](uint32_t b, uint32_t live) {
@@ -217,22 +213,30 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       return key0 + (int32_t)B - 1 > t.p0 || (p.window && key0 <= tfloor1 && key0 + (int32_t)B > sinks);
     };
 
-    // K fragments of tile buffer b: k steps 4 j .. 4 j + 3
-    const uint32_t kbase = l32 * L::kRow, kx = (h ^ kswz(l32)) * 16;
-    short8_t kf[2][4];
-    auto read_k = [&](uint32_t b, int j) {
+    // The lane's places in the ring: K fragments by k step, V by column tile, of the block's first buffer (0 or 2); the
+    // second is an immediate away, and going to the next block's flips one bit.
+    constexpr uint32_t kFlip = 2 * L::kSize;
+    static_assert((kFlip & (kFlip - 1)) == 0, "two buffers are a power of two");
+    const char* const lds = ring[0];
+    uint32_t kat[KS], vat[DT];
+    const uint32_t kx = (h ^ kswz(l32)) * 16;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        kf[j][x] = *reinterpret_cast<const short8_t*>(ring[b] + (kbase + (kx ^ ((4 * j + x) * 32))));
+    for (int k = 0; k < KS; ++k) kat[k] = l32 * L::kRow + (kx ^ (k * 32));
+    short8_t kf[2][4];
+    auto read_k = [&](int second, int j) {     // k steps 4 j .. 4 j + 3 of the block's first or second tile
+#pragma unroll
+      for (int x = 0; x < 4; ++x) kf[j][x] = *reinterpret_cast<const short8_t*>(lds + kat[4 * j + x] + second * L::kSize);
     };
     // V^T fragments of a k step (16 keys), columns 32 d ..: its keys 4 h + (0..3), and 8 further on
     const uint32_t vrow = 4 * h + ((lane & 15) >> 2);
     const uint32_t vx = ((lane & 16) * 2 + (lane & 3) * 8) ^ (vswz(vrow) * 16);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vat[d] = L::kV + vrow * L::kRow + (vx ^ (d * 64));
     short8_t vf[2][DT];
-    auto read_v = [&](uint32_t b, int step_k) {
+    auto read_v = [&](int second, int step_k) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        const char* const a = ring[b] + L::kV + step_k * 16 * L::kRow + (vrow * L::kRow + (vx ^ (d * 64)));
+        const char* const a = lds + vat[d] + second * L::kSize + step_k * 16 * L::kRow;
         vf[step_k][d] = join(read_tr(a), read_tr(a + 8 * L::kRow));
       }
     };
@@ -251,6 +255,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     int32_t sl0 = -1, sl1 = -1, sl2 = -1;    // slots of this window's keys and of the next two's
     uint32_t place = 0;                      // of window w + 2 at the start of window w
     float top = 0.f;
+    float limit = -INFINITY, base = 0.f;     // m + kLag, and -m (0 while nothing is seen)
     if (nblk) {
       const uint32_t p0 = request(0), p1 = request(1);
       place = request(2);
@@ -259,9 +264,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       sl1 = slots(1, p1);
       fetch(0, sl0, 0, 0);
       fetch(1, sl0, 0, 1);
-      fetch(2, pick(!grouped, sl0, sl1, sl1), 1, 0);
-      if (grouped) wait_vm_barrier<4 * NL>();
-      else wait_vm_barrier<4 * NL * RPW>();
+      fetch(2, pick(!kGrouped, sl0, sl1, sl1), 1, 0);
+      wait_vm_barrier<2 * kLoads>();
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[0][e] = 0.f;
 #pragma unroll
@@ -272,22 +276,26 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       top = max_of(s[0]);
     }
 
-    // Tile 2 i + half of the piece; its scores and their maxima are there.  kEdge: some row does not see some key
-    // of the block (of the tile's rows: the choice is the workgroup's).
+    // Tile 2 i + half of the piece; its scores and their maxima are there.  kEdge: some row does
+    // not see some key of the block (of the tile's rows: the choice is the workgroup's).
     auto step = [&](auto edge_tag, auto half_tag, uint32_t i) {
       constexpr bool kEdge = decltype(edge_tag)::value;
       constexpr int kHalf = decltype(half_tag)::value;
-      const uint32_t b = 2 * (i & 1) + kHalf, bn = (b + 1) & 3;
+      const uint32_t b = 2 * (i & 1) + kHalf;
       floatx16& sc = s[kHalf];
       floatx16& sn = s[1 - kHalf];
-      wait_tile();                       // the next tile is in place, the one before this no longer read
-      if (kHalf == 0 && (i & ((1u << ks) - 1)) == 0) {
-        sl2 = slots((i >> ks) + 2, place);
-        place = request((i >> ks) + 3);
+      wait_vm_barrier<kLoads>();         // the next tile is in place, the one before this no longer read
+      if (kHalf == 0 && i % kPer == 0) {
+        sl2 = slots(i / kPer + 2, place);
+        place = request(i / kPer + 3);
       }
-      const uint32_t in = i + 1 + kHalf, wn = (in >> ks) - (i >> ks);   // of the tile three on
-      fetch((b + 3) & 3, pick(wn, sl0, sl1, sl2), in, 1 - kHalf);
-      read_k(bn, 0);
+      const uint32_t in = i + 1 + kHalf;
+      fetch((b + 3) & 3, pick(in / kPer - i / kPer, sl0, sl1, sl2), in, 1 - kHalf);
+      if constexpr (kHalf == 1) {        // the next tile's K is in the next block's buffers
+#pragma unroll
+        for (int k = 0; k < KS; ++k) kat[k] ^= kFlip;
+      }
+      read_k(1 - kHalf, 0);
       bool special = false;
       uint32_t there = 0;
       if constexpr (kEdge) {
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         }
         top = max_of(sc);
       }
-      if (__any(top > m + kLag)) {
+      if (__any(top > limit)) {
         const float m1 = fmaxf(m, top);
         const float old = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
         l *= old;
@@ -315,8 +323,9 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[d][e] *= old;
         m = m1;
+        limit = m + kLag;
+        base = m == -INFINITY ? 0.f : -m;
       }
-      const float base = m == -INFINITY ? 0.f : -m;
       short8_t w[2];
       auto weigh = [&](int step_k) {     // weights of a k step
         u32x4 pk;
@@ -331,26 +340,35 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       };
       // Left alone, the compiler reads each fragment just before its MFMA and waits out the LDS latency every
       // time; the scheduling barriers keep the reads one group of MFMAs ahead.
-      if constexpr (KS > 4) read_k(bn, 1);
-      else read_v(b, 0);
+      if constexpr (KS > 4) read_k(1 - kHalf, 1);
+      else read_v(kHalf, 0);
 #pragma unroll
       for (int e = 0; e < 16; ++e) sn[e] = 0.f;
+      // (One wait per group, by count, instead of one per fragment.)
+      __builtin_amdgcn_sched_barrier(0);
+      wait_lds<(KS > 4 ? 4 : 2 * DT)>();
       __builtin_amdgcn_sched_barrier(0);
       scores(sn, 0);
       weigh(0);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (KS > 4) {
-        read_v(b, 0);
+        read_v(kHalf, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_lds<2 * DT>();
         __builtin_amdgcn_sched_barrier(0);
         scores(sn, 1);
         weigh(1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      read_v(b, 1);
+      read_v(kHalf, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_lds<2 * DT>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[0][d], w[0], o[d]);
       if constexpr (KS <= 4) weigh(1);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_lds<0>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = mfma32<kBf16>(vf[1][d], w[1], o[d]);
@@ -381,6 +399,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
                   const float vv = to_f32<kBf16>((uint16_t)(v[y >> 1] >> (16 * (y & 1))));
                   o[d][4 * k + y] += x != 0.f && !(fabsf(vv) < INFINITY) ? x * vv : 0.f;
                 }
+                __builtin_amdgcn_sched_barrier(0);   // few registers at a time
               }
           }
           wait_vm<0>();   // or the compiler waits for these loads in the common loop
@@ -390,16 +409,18 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     auto block = [&](auto edge_tag, uint32_t i) {
       step(edge_tag, std::integral_constant<int, 0>{}, i);
       step(edge_tag, std::integral_constant<int, 1>{}, i);
-      if (((i + 1) & ((1u << ks) - 1)) == 0) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vat[d] ^= kFlip;
+      if ((i + 1) % kPer == 0) {
         sl0 = sl1;
         sl1 = sl2;
       }
     };
     // every row sees every key of block i, and all are there
-    const uint32_t group_bits = 64u >> ks;
     auto clean = [&](uint32_t i) {
-      const uint64_t absent = __ballot(sl0 < 0) >> ((i & ((1u << ks) - 1)) * group_bits);
-      return !edge_of(key0_of(i)) && (absent << (64 - group_bits)) == 0;
+      constexpr uint32_t bits = 64 >> ks;
+      const uint64_t absent = __ballot(sl0 < 0) >> (i % kPer * bits);
+      return !edge_of(key0_of(i)) && (absent & (~0ull >> (64 - bits))) == 0;
     };
     for (uint32_t i = 0; i < nblk;) {
       for (; i < nblk && !clean(i); ++i) block(std::true_type{}, i);
@@ -452,15 +473,19 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 
 hipError_t launch_attention_tile(const PagedAttention& p, const AttentionPlan& plan, hipStream_t stream) {
   const size_t lds = plan.split ? sizeof(Line) : 0;
-#define KAIO_TILE(BF, DIM)                                                                                   \
-  hipLaunchKernelGGL((attention_tile_kernel<BF, DIM>), dim3(plan.workgroups), dim3(256), lds, stream, p,     \
-                     plan.split, plan.tiles)
+  const uint64_t cache = (uint64_t)p.kv.pages * p.kv.page.d * p.kv.kv_heads * p.kv.head_dim * 2;
+  const bool grouped = p.kv.page.d % (p.kv.head_dim == 128 ? 4 : 8) == 0 && cache <= 0xFFFFFFFFull;
+#define KAIO_TILE(BF, DIM)                                                                                      \
+  if (grouped)                                                                                                  \
+    hipLaunchKernelGGL((attention_tile_kernel<BF, DIM, true>), dim3(plan.workgroups), dim3(256), lds, stream,   \
+                       p, plan.split, plan.tiles);                                                              \
+  else                                                                                                          \
+    hipLaunchKernelGGL((attention_tile_kernel<BF, DIM, false>), dim3(plan.workgroups), dim3(256), lds, stream,  \
+                       p, plan.split, plan.tiles)
   if (p.kv.head_dim == 128) {
-    if (p.bf16) KAIO_TILE(true, 128);
-    else KAIO_TILE(false, 128);
+    if (p.bf16) { KAIO_TILE(true, 128); } else { KAIO_TILE(false, 128); }
   } else {
-    if (p.bf16) KAIO_TILE(true, 64);
-    else KAIO_TILE(false, 64);
+    if (p.bf16) { KAIO_TILE(true, 64); } else { KAIO_TILE(false, 64); }
   }
 #undef KAIO_TILE
   return hipGetLastError();
