@@ -187,17 +187,14 @@ __device__ __forceinline__ float* partial_of(const PagedAttention& p, uint32_t w
   return reinterpret_cast<float*>(static_cast<JoinNote*>(p.workspace) + workers) + (size_t)slot * (R * (D + 2));
 }
 
-// Zeros for the rows of q that no sequence has: before q_start[0] and from
-// q_start[seqs] on.  (At a kernel's end, where its loads wait for nobody.)
-__device__ __forceinline__ void zero_unowned(const PagedAttention& p, uint32_t wg, uint32_t wgs) {
+// Zeros for the rows of q that no sequence has: outside [a, b).
+__device__ __forceinline__ void zero_unowned(const PagedAttention& p, uint32_t wg, uint32_t wgs, uint32_t a, uint32_t b) {
   const uint32_t T = p.kv.tokens;
-  const uint32_t a = p.kv.seqs ? (uint32_t)clamp_row(p.kv.q_start[0], T) : T;
-  uint32_t b = p.kv.seqs ? (uint32_t)clamp_row(p.kv.q_start[p.kv.seqs], T) : T;
   if (a == 0 && b == T) return;
   const uint32_t row = p.q_heads * p.kv.head_dim;
   for (uint32_t t = wg; t < T; t += wgs) {
     if (t >= a && t < b) {
-      t += (b - 1 - t) / wgs * wgs;   // skip the owned rows
+      t += (b - 1 - t) / wgs * wgs;   // skip the others
       continue;
     }
     for (uint32_t e = threadIdx.x * 8; e < row; e += blockDim.x * 8)

@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
     first_piece = false;
   }
   walk.leave_note();
-  zero_unowned(p, blockIdx.x, gridDim.x);
+  uint32_t own_a, own_b;
+  walk.owned(own_a, own_b);
+  zero_unowned(p, blockIdx.x, gridDim.x, own_a, own_b);
 }
 
 }  // namespace

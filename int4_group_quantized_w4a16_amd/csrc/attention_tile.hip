@@ -466,7 +466,9 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     }
   }
   walk.leave_note();
-  zero_unowned(p, blockIdx.x, gridDim.x);
+  uint32_t own_a, own_b;
+  walk.owned(own_a, own_b);
+  zero_unowned(p, blockIdx.x, gridDim.x, own_a, own_b);
 }
 
 }  // namespace

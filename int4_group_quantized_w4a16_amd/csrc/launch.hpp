@@ -256,7 +256,9 @@ constexpr AttentionPlan attention_plan(uint32_t kv_heads, uint32_t q_heads, uint
   // every sequence's last tile may be short
   const uint64_t tiles = tokens * g / rows + seqs;
   a.tiles = tiles ? (uint32_t)tiles : 1;
-  const uint64_t slots = 2 * kComputeUnits;                 // workgroups resident at once
+  // workgroups resident at once (three of the tile form's at 64 columns would fit: 80.4 us against 77.3 for 2049
+  // windowed rows of 16 heads, as more workgroups mean more pieces)
+  const uint64_t slots = 2 * kComputeUnits;
   a.split = tiles <= kSchedTiles && a.tiles * kv_heads < 4 * slots && (cap / keys + 2) * a.tiles * kv_heads < (1ull << 31);
   a.workgroups = (uint32_t)(a.split ? slots : a.tiles * kv_heads);
   a.workspace = a.split ? slots * (32 + 2 * rows * (head_dim + 2) * 4) : 0;
