@@ -107,3 +107,38 @@ def test_graph_replays():
         want = kaio.kaio_rope_append(b.dq, k, v, pos, inv, [64], b.paged)
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(got_k, b.dk)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,sections,tokens", [(4, 2, 64, [8, 8, 16], 2055), (4, 4, 64, [32], 1031), (2, 1, 16, [8], 2050),
+                                                      (1, 1, 40, [8], 3001)])
+def test_several_tokens_per_workgroup(hq, hkv, d, sections, tokens, interleaved):
+    # more tokens than workgroups, a last workgroup that is not full, sequences that end inside one, slots that are missing
+    new = [tokens - 13, 3, 0, 6]
+    b = Batch(new, [tokens - 13 + 8, 40, 5, 6], hq, hkv, d, 16, "bf16", seed=tokens, pad=4)
+    b.table[0, 5] = -1
+    b.table[1, 2] = b.pages
+    run_case(b, sections, interleaved, spread(b, len(sections)))
+
+
+def test_large_offsets():
+    # a cache of more than 2^32 bytes: the slots at its far end, with one token and several per workgroup
+    page, hkv, d = 64, 8, 128
+    pages = (2 ** 32 // (page * hkv * d * 2)) + 60
+    k = torch.zeros((pages, page, hkv, d), dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    inv = torch.tensor([1e4 ** (-j / 64) for j in range(64)], dtype=torch.float64, device=DEV)
+    for new, hq in ((9, 8), (2050, 8)):
+        small = Batch([new], [new + 100], hq, hkv, d, page, "f16", seed=new)
+        small.on_gpu()
+        dk, dv, pos = small.k.to(DEV), small.v.to(DEV), spread(small, 1).to(DEV)
+        far = pages - small.pages
+        k[far:].copy_(small.dk)
+        v[far:].copy_(small.dv)
+        want = kaio.kaio_rope_append(small.dq, dk, dv, pos, inv, [64], small.paged)
+        table = torch.where(small.table >= 0, small.table + far, small.table)
+        there = kaio.KaioPagedKV(k, v, table.to(DEV), small.paged.q_start, small.paged.lens)
+        got = kaio.kaio_rope_append(small.dq, dk, dv, pos, inv, [64], there)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(k[far:], small.dk) and torch.equal(v[far:], small.dv)
+    del k, v
