@@ -242,3 +242,59 @@ def test_large_offsets():
     torch.cuda.synchronize()
     assert torch.equal(ref, out)
     del k, v
+
+
+@pytest.mark.parametrize("new,heads", [(90, 8), (200, 8)])
+def test_large_offsets_of_chunks(new, heads):
+    # a cache of more than 2^32 bytes under tiles of many rows
+    page, hkv, d = 64, 8, 128
+    pages = (2 ** 32 // (page * hkv * d * 2)) + 40
+    small = Batch([new], [300], heads, hkv, d, page, "f16", seed=new)
+    small.check(small.attention())
+    k = torch.zeros((pages, page, hkv, d), dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    far = pages - small.pages
+    k[far:].copy_(small.dk)
+    v[far:].copy_(small.dv)
+    table = torch.where(small.table >= 0, small.table + far, small.table)
+    paged = kaio.KaioPagedKV(k, v, table.to(DEV), small.q_start.to(DEV), torch.tensor([300], dtype=torch.int32, device=DEV))
+    out = kaio.kaio_paged_attention(small.dq, paged, new, small.scale)
+    torch.cuda.synchronize()
+    small.check(out)
+    del k, v
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [1, 2, 3, 5, 12, 20])
+def test_page_sizes_of_chunks(page, d):
+    # pages that end anywhere in a tile, for tiles of many rows, with a window
+    b = Batch([70, 1, 33], [240, 65, 33], 4, 2, d, page, "bf16", seed=page + d)
+    b.check(b.attention())
+    b = Batch([45, 140], [400, 333], 6, 2, d, page, "f16", seed=page, window=50, sinks=5)
+    b.check(b.attention())
+
+
+@pytest.mark.parametrize("page", [3, 16])
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+def test_what_invisible_slots_hold_does_not_matter_at_128(page, new, bad):
+    b = Batch([new, new], [203, 90], 4, 2, 128, page, "bf16", seed=4, window=50, sinks=3)
+    ref = b.attention()
+    b.check(ref)
+    hide = ~b.used()
+    for c in (b.k_cache, b.v_cache):
+        c.view(-1, *c.shape[2:])[hide] = bad
+    assert torch.equal(ref, b.attention())
+
+
+def test_tensors_that_are_not_contiguous_and_the_checked_path():
+    # an explicit stream takes the wrapper's checked path: the same bits; strided views of q are refused
+    b = Batch([1, 9], [70, 40], 8, 2, 128, 16, "f16", seed=21)
+    ref = b.attention()
+    for out in (kaio.kaio_paged_attention(b.dq, b.paged, 9, b.scale),
+                kaio.kaio_paged_attention(b.dq, b.paged, 9, b.scale, stream=torch.cuda.current_stream())):
+        torch.cuda.synchronize()
+        assert torch.equal(ref, out)
+    wide = torch.cat([b.dq, b.dq], 1)
+    with pytest.raises(ValueError, match="contiguous"):
+        kaio.kaio_paged_attention(wide[:, ::2], b.paged, 9, b.scale)
