@@ -83,6 +83,13 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // rare after the first blocks.  The result is the same quotient.
 constexpr float kLag = 8.0f;
 
+// Added to every weight's exponent, so that f16, whose normal numbers end at
+// 2^-14, keeps all bits of weights down to 2^-21 of the largest and rounds only
+// those under 2^-32 of it to zero (of a long axis they could be many).  With
+// kLag the largest weight is 2^15.  bf16 has f32's range.
+template <bool kBf16>
+constexpr float kLift = kBf16 ? 0.0f : 7.0f;
+
 // Non-finite 16-bit values in a dword (any half with all exponent bits set).
 template <bool kBf16>
 __device__ __forceinline__ bool any_special(uint32_t w) {

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
             for (int e = 0; e < 4; ++e) o[d][e] *= old;
           m = m1;
         }
-        const float base = m == -INFINITY ? 0.f : -m;
+        const float base = m == -INFINITY ? 0.f : kLift<kBf16> - m;
         u32x4 pk;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {

@@ -298,3 +298,27 @@ def test_tensors_that_are_not_contiguous_and_the_checked_path():
     wide = torch.cat([b.dq, b.dq], 1)
     with pytest.raises(ValueError, match="contiguous"):
         kaio.kaio_paged_attention(wide[:, ::2], b.paged, 9, b.scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_long_tail_of_small_weights_counts(new, dtype, d):
+    # one key of weight 1 and V = 0, thousands of weight 2^-20.4 and V = 1: their mean is all of the result.  Weights
+    # that small keep their bits: half a step for each weight and half a step for the output
+    b = Batch([new], [3000], 2, 1, d, 64, dtype, seed=22)
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k_cache.zero_()
+    b.k_cache[..., 0] = -20.4
+    b.v_cache.fill_(1.0)
+    first = b.table[0, 0]
+    b.k_cache[first, 0, :, 0] = 0.0
+    b.v_cache[first, 0] = 0.0
+    b.scale = float(np.log(2.0))
+    out = f64(b.attention())
+    w = 2.0 ** f64(b.k_cache[first, 1, 0, :1])[0]
+    seen = np.arange(3000 - new, 3000)                  # keys of small weight each row sees
+    want = (seen * w / (1 + seen * w))[:, None, None]
+    half = 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
+    assert (np.abs(out - want) <= 2 * half * 1.01 * want).all()
