@@ -354,6 +354,8 @@ kaio_status kaio_rope_append(const kaio_paged_kv* kv, const void* q, const void*
  * lens[s], its page there, and, with window > 0, c > pos - window or c < sinks.
  * A row that sees nothing is zero.  Scores, softmax and sums are f32.
  * Invisible positions are not read into the result, whatever they hold.
+ * Scores of a magnitude past 2^26, where f32's steps exceed the weights'
+ * range, may make their row NaN.
  *
  *   q, out  [tokens, q_heads, head_dim]
  *   max_new    the most new tokens a sequence has (it chooses the kernel; a

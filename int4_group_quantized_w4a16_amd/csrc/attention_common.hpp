@@ -78,15 +78,16 @@ __device__ __forceinline__ float add_rows16(float x) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The running maximum may lag behind the true one by this much (in powers of
-// two) before the sums are rescaled: weights then reach 2^8 instead of 1, far
-// inside f16's range, and rescaling, which touches every accumulator, becomes
-// rare after the first blocks.  The result is the same quotient.
-constexpr float kLag = 8.0f;
+// two) before the sums are rescaled: weights then reach 2^5 instead of 1, and
+// rescaling, which touches every accumulator, becomes rare after the first
+// blocks.  The result is the same quotient.
+constexpr float kLag = 5.0f;
 
 // Added to every weight's exponent, so that f16, whose normal numbers end at
 // 2^-14, keeps all bits of weights down to 2^-21 of the largest and rounds only
 // those under 2^-32 of it to zero (of a long axis they could be many).  With
-// kLag the largest weight is 2^15.  bf16 has f32's range.
+// kLag the largest weight is 2^12; f16 ends at 2^16, which leaves room for the
+// steps of f32 in a score, up to 4 for scores of 2^26.  bf16 has f32's range.
 template <bool kBf16>
 constexpr float kLift = kBf16 ? 0.0f : 7.0f;
 

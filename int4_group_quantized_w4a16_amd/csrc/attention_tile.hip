@@ -250,11 +250,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 #pragma unroll
       for (int x = 0; x < 4; ++x) sc = mfma32<kBf16>(kf[j][x], q[4 * j + x], sc);
     };
-    auto max_of = [&](const floatx16& sc) {
+    auto max_of = [&](const floatx16& sc) {   // of this lane's half of the row, unscaled
       float top = sc[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, sc[e]);
-      return max_halves(top) * c;
+      return top;
     };
 
     int32_t sl0 = -1, sl1 = -1, sl2 = -1;    // slots of this window's keys and of the next two's
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         }
         top = max_of(sc);
       }
-      if (__any(top > limit)) {
-        const float m1 = fmaxf(m, top);
+      if (__any(top * c > limit)) {      // the row's maximum, over both halves, only where it matters
+        const float m1 = fmaxf(m, max_halves(top) * c);
         const float old = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
         l *= old;
 #pragma unroll

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import int4_group_quantized_w4a16_amd as kaio
+from oracle import paged
 from tests.gpu_util import DEV
 from tests.paged_util import Batch, f64
 
@@ -322,3 +323,25 @@ def test_a_long_tail_of_small_weights_counts(new, dtype, d):
     want = (seen * w / (1 + seen * w))[:, None, None]
     half = 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
     assert (np.abs(out - want) <= 2 * half * 1.01 * want).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("size", [1e3, 1e5, 3e6, 2e7])
+def test_large_equal_scores_weigh_alike(size, new, dtype, d):
+    # every key has the same score, far from zero on either side: the result is the mean of V over what the row sees.
+    # Equal scores give equal weights, whatever f32's steps at that size are: half a step of the output, half a step of
+    # the mean (weights that do not round alike in value but alike for all), and the sums' 2 n roundings
+    for sign in (1.0, -1.0):
+        b = Batch([new], [300], 2, 1, d, 16, dtype, seed=23)
+        b.q.zero_()
+        b.q[:, :, 0] = 1.0
+        b.k_cache.zero_()
+        b.k_cache[..., 0] = sign * 1000.0
+        b.scale = size / 1000.0
+        y, terms = paged.attention(f64(b.q), f64(b.k_cache), f64(b.v_cache), b.table.numpy(), b.q_start.numpy(), b.lens,
+                                   b.scale)
+        eps, low = (2.0 ** -10, 2.0 ** -14) if dtype == "f16" else (2.0 ** -7, 2.0 ** -126)
+        tol = eps / 2 * np.abs(y) + (eps / 2 + 2 * 308 * 2.0 ** -24) * terms[0] + eps * low / 2 * 301
+        assert (np.abs(f64(b.attention()) - y) <= tol).all()
