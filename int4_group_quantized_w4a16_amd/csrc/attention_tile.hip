@@ -43,6 +43,16 @@
 //   the latter are added to the rows that see them afterwards, one by one.
 //   Such blocks run in a loop of their own, so that the common one is small
 //   and keeps its accumulators in place.
+// * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 586 us, 938
+//   TFLOP/s.  1535 rows of three sequences over 4000 to 12000 cached keys, 32
+//   heads over 8: 247 us with the join (13), 819.  2049 rows of 16 heads of 64
+//   columns in a window of 4096: 76 us with the join (8), 454.  Of the first
+//   case's time 421 us remain without the softmax and 388 without the MFMAs
+//   (half of the cycles are the MFMAs' own): what bounds it is how far the two
+//   waves of a SIMD overlap.  Slower: 64 rows per wave with one wave per SIMD
+//   (836 us), eight waves in a workgroup, the halves kept half a step apart by
+//   barriers (744) or not (629), K fragments read a step ahead (+1%), V of
+//   edge tiles cleaned a tile ahead without a barrier of its own (+2%).
 
 #include <type_traits>
 
