@@ -31,7 +31,7 @@ static_assert(R == 16 && B == 4 * kKeys, "four waves of 32 keys, 16 rows");
 
 template <int D>
 struct Lds {
-  static constexpr int kKRow = D * 2 + 16;   // padded as in the tile form
+  static constexpr int kKRow = D * 2 + 16;   // 16 bytes more than a multiple of the banks: rows lie apart
   static constexpr int kVRow = D * 2;
   static constexpr int kK = kKeys * kVRow;   // V first (its swizzle wants aligned rows)
   static constexpr int kSize = kK + kKeys * kKRow;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
         if (!special) {
 #pragma unroll
           for (int d = 0; d < DT; ++d) o[d] = mfma16<kBf16>(vfrag(d), w, o[d]);
-        } else {   // as in the tile form
+        } else {   // non-finite values apart, as counts of those that a row sees: weight 0 times infinity is not 0
           constexpr short one = kBf16 ? 0x3F80 : 0x3C00;
           short8_t sees;
 #pragma unroll

@@ -38,15 +38,17 @@
 //   mostly in its second product, which needs few issue slots (8192 causal
 //   keys: 612 us without, 592 with).
 // * Masks are applied only in blocks that some row does not wholly see, by
-//   selects on scores.  In those blocks a pass over V in LDS zeroes slots that
-//   are not there and non-finite values (weight 0 times infinity is not 0);
-//   the latter are added to the rows that see them afterwards, one by one.
-//   Such blocks run in a loop of their own, so that the common one is small
-//   and keeps its accumulators in place.
+//   selects on scores, from the set of keys that the lane's row sees as the
+//   bits of a word (comparing key by key: 75.8 us for the windowed case below,
+//   69.1 so).  In those blocks a pass over V in LDS zeroes slots that are not
+//   there and non-finite values (weight 0 times infinity is not 0); the latter
+//   are added to the rows that see them afterwards, one by one.  Such blocks
+//   run in a loop of their own, so that the common one is small and keeps its
+//   accumulators in place.
 // * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 586 us, 938
 //   TFLOP/s.  1535 rows of three sequences over 4000 to 12000 cached keys, 32
 //   heads over 8: 247 us with the join (13), 819.  2049 rows of 16 heads of 64
-//   columns in a window of 4096: 76 us with the join (8), 454.  Of the first
+//   columns in a window of 4096: 70 us with the join (8), 490.  Of the first
 //   case's time 421 us remain without the softmax and 388 without the MFMAs
 //   (half of the cycles are the MFMAs' own): what bounds it is how far the two
 //   waves of a SIMD overlap.  Slower: 64 rows per wave with one wave per SIMD
@@ -318,15 +320,13 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         const int32_t mine = __shfl(sl0, (int)slot_lane(i, 32 * kHalf + l32));
         there = (uint32_t)__ballot(mine >= 0 && tile0 + (int32_t)l32 < t.hi);
         special = fix_v(b, there);
-        const uint32_t bits = there >> (4 * h);
-        const int32_t key0 = tile0 + 4 * (int32_t)h;
+        // the keys of the tile that this lane's row sees, bit by bit: there, c <= pos, and c > floor or c < sinks
+        auto first = [](int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };   // n ones
+        const uint32_t bits =
+            (there & first(pos - tile0 + 1) & (~first(floor - tile0 + 1) | first(sinks - tile0))) >> (4 * h);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int off = 8 * (e / 4) + e % 4;
-          const int32_t key = key0 + off;
-          const bool sees = key <= pos && (key > floor || key < sinks) && ((bits >> off) & 1);
-          sc[e] = sees ? sc[e] : -INFINITY;
-        }
+        for (int e = 0; e < 16; ++e)
+          sc[e] = (int32_t)(bits << (31 - (8 * (e / 4) + e % 4))) < 0 ? sc[e] : -INFINITY;
         top = max_of(sc);
       }
       if (__any(top * c > limit)) {      // the row's maximum, over both halves, only where it matters

@@ -1,5 +1,5 @@
 // The paged key/value cache as the kernels see it, shared by rope_append.hip
-// and paged_attention.hip.
+// and the attention kernels.
 //
 // A batch holds `seqs` sequences.  Sequence s has new tokens in rows
 // q_start[s] .. q_start[s+1] of q and lens[s] tokens in the cache, the new
