@@ -73,9 +73,6 @@ struct Lds {
   static constexpr int kSize = 2 * kV;
 };
 
-// by value: a choice between variables would keep them, and what is captured with them, in memory
-__device__ __forceinline__ int32_t pick(uint32_t i, int32_t a, int32_t b, int32_t c) { return i == 0 ? a : i == 1 ? b : c; }
-
 // kGrouped: keys that a load covers share a page, so one slot, a scalar offset, serves them all (and the offsets of
 // the cache fit in 32 bits).  Otherwise a load per key.
 template <bool kBf16, int D, bool kGrouped>
@@ -180,8 +177,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       koff[n] = off + (lch ^ kswz(row)) * 16;
       voff[n] = off + (lch ^ vswz(row)) * 16;
     }
-    auto fetch = [&](uint32_t b, int32_t slot, uint32_t i, int half) {
-      const int32_t there = slot < 0 ? 0 : slot;
+    auto fetch = [&](uint32_t b, int32_t there, uint32_t i, int half) {   // there: slots, 0 for absent ones
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const uint32_t row0 = (4 * n + wave) * RPW;
@@ -270,6 +266,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     };
 
     int32_t sl0 = -1, sl1 = -1, sl2 = -1;    // slots of this window's keys and of the next two's
+    int32_t slf = 0;                         // slots of the window that is fetched from, 0 for absent ones
     uint32_t place = 0;                      // of window w + 2 at the start of window w
     float top = 0.f;
     float limit = -INFINITY, base = 0.f;     // m + kLag, and kLift - m (0 while nothing is seen)
@@ -279,9 +276,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       wait_vm<0>();   // the ids are the wave's own
       sl0 = slots(0, p0);
       sl1 = slots(1, p1);
-      fetch(0, sl0, 0, 0);
-      fetch(1, sl0, 0, 1);
-      fetch(2, pick(!kGrouped, sl0, sl1, sl1), 1, 0);
+      slf = max(sl0, 0);
+      fetch(0, slf, 0, 0);
+      fetch(1, slf, 0, 1);
+      if constexpr (kPer == 1) slf = max(sl1, 0);
+      fetch(2, slf, 1, 0);
       wait_vm_barrier<2 * kLoads>();
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[0][e] = 0.f;
@@ -306,8 +305,11 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         sl2 = slots(i / kPer + 2, place);
         place = request(i / kPer + 3);
       }
-      const uint32_t in = i + 1 + kHalf;
-      fetch((b + 3) & 3, pick(in / kPer - i / kPer, sl0, sl1, sl2), in, 1 - kHalf);
+      const uint32_t in = i + 1 + kHalf;     // its first half is fetched now (kHalf 1), or its second
+      if constexpr (kHalf == 1) {
+        if (in % kPer == 0) slf = max(kPer == 1 ? sl2 : sl1, 0);
+      }
+      fetch((b + 3) & 3, slf, in, 1 - kHalf);
       if constexpr (kHalf == 1) {        // the next tile's K is in the next block's buffers
 #pragma unroll
         for (int k = 0; k < KS; ++k) kat[k] ^= kFlip;
