@@ -23,8 +23,9 @@
 // The lengths are only known on the device, so every workgroup derives the
 // line from them by itself (2 us; it needs one load of each array).
 //
-// Direct form, for calls with so many tiles that they balance by themselves:
-// one workgroup per tile and K/V head, nothing to join.
+// Direct form, for calls with so many tiles that they balance by themselves or
+// so few blocks that it does not matter (attention_direct in launch.hpp): one
+// workgroup per tile and K/V head, nothing to join.
 #pragma once
 
 #include "common.hpp"

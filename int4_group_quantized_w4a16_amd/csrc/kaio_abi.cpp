@@ -307,9 +307,10 @@ kaio::PagedKV paged_of(const kaio_paged_kv* kv, uint32_t tokens) {
   return p;
 }
 
-kaio::AttentionPlan attention_plan_of(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads, uint32_t max_new) {
+kaio::AttentionPlan attention_plan_of(const kaio_paged_kv* kv, uint32_t tokens, uint32_t q_heads, uint32_t max_new,
+                                      uint32_t window = 0, uint32_t sinks = 0) {
   return kaio::attention_plan(kv->kv_heads, q_heads, kv->head_dim, kv->seqs,
-                              (uint64_t)kv->table_width * kv->page_size, tokens, max_new);
+                              (uint64_t)kv->table_width * kv->page_size, tokens, max_new, window, sinks);
 }
 
 }  // namespace
@@ -587,7 +588,7 @@ kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* o
     return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, q_heads=%u, seqs=%u, slots=%llu)",
                 tokens, q_heads, kv->seqs, (unsigned long long)kv->pages * kv->page_size);
   if (kaio_status st = check_paged_pointers(op, kv)) return st;
-  const kaio::AttentionPlan plan = attention_plan_of(kv, tokens, q_heads, max_new);
+  const kaio::AttentionPlan plan = attention_plan_of(kv, tokens, q_heads, max_new, window, sinks);
   const uint64_t need = plan.workspace;
   if (!q) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input q is null");
   if (!out) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output out is null");

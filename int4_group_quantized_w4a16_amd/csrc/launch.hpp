@@ -245,8 +245,22 @@ struct AttentionPlan {
   uint32_t workgroups;
   uint64_t workspace;       // bytes
 };
+// Whether few enough blocks leave nothing to gain from splitting tiles: one workgroup takes a tile from end to end, with
+// no schedule to derive and nothing to join.  blocks: a bound on a tile's; share: tiles over workgroups resident at
+// once.  A tile's block takes `alone` us with one workgroup on a compute unit, a split call `base` us more than a direct
+// one and `full` us per block and resident workgroup (the mean tile of a prompt has half of the last one's blocks).  us,
+// split / direct: 1024 tokens of 32 heads over 8, causal, 49 / 28; 4096 tokens 233 / 156; 1024 over 1024 58 / 46; 33 over
+// 2000 28 / 45; 300 over 1000 39 / 34 (split all the same); decode over 8 x 250 keys 12.8 / 8.5, 64 x 500 22.9 / 18.0,
+// 16 x 900 15.2 / 21.4.  Past `most` blocks lengths that differ would leave too much to single workgroups.
+// If it holds for a number of blocks, it holds for fewer.
+constexpr bool attention_direct(bool stream, uint32_t head_dim, double blocks, double share, double mean) {
+  const double alone = stream ? 2.0 : head_dim == 128 ? 1.24 : 0.85, full = stream ? 2.0 : head_dim == 128 ? 2.5 : 1.7;
+  const double base = stream ? 7.0 : 14.0, most = stream ? 4.0 : 64.0;
+  return blocks <= most && blocks * (alone - full * share * mean) <= base;
+}
+// window 0 and sinks 0 give a workspace that is enough with any.
 constexpr AttentionPlan attention_plan(uint32_t kv_heads, uint32_t q_heads, uint32_t head_dim, uint32_t seqs,
-                                       uint64_t cap, uint32_t tokens, uint32_t max_new) {
+                                       uint64_t cap, uint32_t tokens, uint32_t max_new, uint32_t window, uint32_t sinks) {
   AttentionPlan a{};
   a.rows = head_dim != 64 && head_dim != 128;
   if (a.rows) return a;
@@ -259,7 +273,17 @@ constexpr AttentionPlan attention_plan(uint32_t kv_heads, uint32_t q_heads, uint
   // workgroups resident at once (three of the tile form's at 64 columns would fit: 80.4 us against 77.3 for 2049
   // windowed rows of 16 heads, as more workgroups mean more pieces)
   const uint64_t slots = 2 * kComputeUnits;
-  a.split = tiles <= kSchedTiles && a.tiles * kv_heads < 4 * slots && (cap / keys + 2) * a.tiles * kv_heads < (1ull << 31);
+  uint64_t blocks = (cap + keys - 1) / keys;
+  double mean = cap > max_new ? 1.0 - 0.5 * max_new / (double)cap : 0.5;
+  if (window) {   // the sinks' blocks, and those of the window before each row of a tile
+    const uint64_t seen = (sinks + keys - 1) / keys + (window + rows / g + keys - 1) / keys + 1;
+    if (seen < blocks) {
+      blocks = seen;
+      mean = 1.0;
+    }
+  }
+  const bool direct = attention_direct(a.stream, head_dim, (double)blocks, (double)a.tiles * kv_heads / slots, mean);
+  a.split = !direct && tiles <= kSchedTiles && a.tiles * kv_heads < 4 * slots && (cap / keys + 2) * a.tiles * kv_heads < (1ull << 31);
   a.workgroups = (uint32_t)(a.split ? slots : a.tiles * kv_heads);
   a.workspace = a.split ? slots * (32 + 2 * rows * (head_dim + 2) * 4) : 0;
   return a;

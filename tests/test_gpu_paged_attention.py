@@ -345,3 +345,26 @@ def test_large_equal_scores_weigh_alike(size, new, dtype, d):
         eps, low = (2.0 ** -10, 2.0 ** -14) if dtype == "f16" else (2.0 ** -7, 2.0 ** -126)
         tol = eps / 2 * np.abs(y) + (eps / 2 + 2 * 308 * 2.0 ** -24) * terms[0] + eps * low / 2 * 301
         assert (np.abs(f64(b.attention()) - y) <= tol).all()
+
+
+@pytest.mark.parametrize("extra", [1, 700])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (6, 2, 64), (8, 1, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [300, 65, 1]), ([130], [333]), ([70, 1, 40, 0], [190, 64, 301, 20])])
+def test_narrow_and_wide_tables(new, lens, hq, hkv, d, window, sinks, extra):
+    # a table with room for much longer sequences splits the keys of a tile over workgroups, a narrow one does not
+    b = Batch(new, lens, hq, hkv, d, 16, "f16", seed=extra + hq, window=window, sinks=sinks, pad=2, extra_width=extra)
+    b.check(b.attention())
+
+
+def test_a_window_needs_no_more_workspace():
+    # the workspace is asked for without the window: a call with one takes it
+    import ctypes
+    from tests.test_paged_host import paged as cache
+    size = kaio.lib().kaio_paged_attention_workspace_size
+    b = Batch([1, 1], [900, 700], 8, 2, 128, 16, "f16", seed=24, window=64, sinks=2, extra_width=50)
+    b.on_gpu()
+    need = size(b.paged._ref, 2, 8, 1)
+    assert need > 0 and size(ctypes.byref(cache(table_width=4)), 3, 4, 1) == 0
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    b.check(b.attention(workspace=ws))
