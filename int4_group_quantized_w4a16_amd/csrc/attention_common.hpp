@@ -195,6 +195,14 @@ __device__ __forceinline__ float* partial_of(const PagedAttention& p, uint32_t w
   return reinterpret_cast<float*>(static_cast<JoinNote*>(p.workspace) + workers) + (size_t)slot * (R * (D + 2));
 }
 
+// Where the tile form puts columns col .. col + 3 of row r of a partial result:
+// as its lanes hold them, so that each store of a wave is one piece of 1 KiB
+// (row by row its 64 lanes wrote 16 bytes each to 32 rows).
+template <int D>
+__device__ __forceinline__ uint32_t fragment_of(uint32_t r, uint32_t col) {
+  return ((r / 32 * (D / 32) + col / 32) * 4 + col % 32 / 8) * 256 + (col % 8 / 4 * 32 + r % 32) * 4;
+}
+
 // Zeros for the rows of q that no sequence has: outside [a, b).
 __device__ __forceinline__ void zero_unowned(const PagedAttention& p, uint32_t wg, uint32_t wgs, uint32_t a, uint32_t b) {
   const uint32_t T = p.kv.tokens;

@@ -6,28 +6,42 @@
 //
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max m_i.
 //
-// One workgroup per note and RPB rows, four columns per thread.  Few rows
-// (decode: the pieces are many, the rows few) leave threads over: they take
-// the pieces in turns, and the partial sums meet in LDS, in a fixed order.
+// Four columns per thread.  Tile form: a workgroup per note, 32 rows and 32
+// columns, threads in the order of the pieces' layout (fragment_of).  Stream
+// form: a workgroup per note, RPB rows at a time; few rows (decode: the pieces
+// are many, the rows few) leave threads over: they take the pieces in turns, and
+// the partial sums meet in LDS, in a fixed order.
 
 #include "attention_common.hpp"
 
 namespace kaio {
 namespace {
 
+template <int D, uint32_t R, uint32_t THREADS>
+constexpr uint32_t groups_of() {   // workgroups per note
+  if (R == kTileRows) return R / 32 * (D / 32);
+  constexpr uint32_t rpb = THREADS / (D / 4);
+  return R > rpb ? R / rpb : 1;
+}
+
 template <bool kBf16, int D, uint32_t R, uint32_t THREADS>
 __global__ void __launch_bounds__(THREADS) attention_join_kernel(PagedAttention p, uint32_t workers) {
-  constexpr uint32_t TPR = D / 4;                           // threads per row
+  constexpr bool kFragments = R == kTileRows;
+  static_assert(!kFragments || THREADS == 256, "32 rows of 8 x 4 columns");
+  constexpr uint32_t TPR = kFragments ? 8 : D / 4;          // threads per row
   constexpr uint32_t RPB = THREADS / TPR;                   // rows per workgroup
-  constexpr uint32_t GROUPS = R > RPB ? R / RPB : 1;
+  constexpr uint32_t GROUPS = groups_of<D, R, THREADS>();
   __shared__ floatx4 part_o[THREADS];
   __shared__ float part_m[RPB], part_l[RPB];
-  const uint32_t tid = threadIdx.x, w = blockIdx.x / GROUPS, row0 = blockIdx.x % GROUPS * RPB;
+  const uint32_t tid = threadIdx.x, w = blockIdx.x / GROUPS, part_id = blockIdx.x % GROUPS;
+  const uint32_t row0 = (kFragments ? part_id / (D / 32) : part_id) * RPB;
   const JoinNote note = static_cast<const JoinNote*>(p.workspace)[w];
   if (note.more == 0 || row0 >= note.rows) return;
   const uint32_t rows = note.rows - row0 < RPB ? note.rows - row0 : RPB;
-  const uint32_t turns = RPB / rows;                        // threads' turns at the pieces
-  const uint32_t rg = tid / TPR, col = tid % TPR * 4;
+  const uint32_t turns = kFragments ? 1 : RPB / rows;       // threads' turns at the pieces
+  const uint32_t rg = kFragments ? tid % 32 : tid / TPR;
+  const uint32_t col = kFragments ? part_id % (D / 32) * 32 + tid / 32 * 4 : tid % TPR * 4;
+  if (kFragments && rg >= rows) return;
   const uint32_t row = row0 + rg % rows, turn = rg / rows;
   float m = -INFINITY, l = 0.f;
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -35,7 +49,7 @@ __global__ void __launch_bounds__(THREADS) attention_join_kernel(PagedAttention 
 #pragma unroll 4
     for (uint32_t i = turn; i <= note.more; i += turns) {
       const float* const part = partial_of<R, D>(p, workers, i == 0 ? 2 * w + 1 : 2 * (w + i));
-      const floatx4 v = *reinterpret_cast<const floatx4*>(part + (size_t)row * D + col);
+      const floatx4 v = *reinterpret_cast<const floatx4*>(part + (kFragments ? fragment_of<D>(row, col) : row * D + col));
       const float mi = part[R * D + row], li = part[R * D + R + row];
       const float m1 = fmaxf(m, mi), base = m1 == -INFINITY ? 0.f : m1;
       const float fo = exp2_fast(m - base), fi = exp2_fast(mi - base);
@@ -78,7 +92,7 @@ __global__ void __launch_bounds__(THREADS) attention_join_kernel(PagedAttention 
 template <bool kBf16, int D, uint32_t R>
 void launch(const PagedAttention& p, uint32_t workers, hipStream_t stream) {
   constexpr uint32_t threads = R == kStreamRows ? 1024 : 256;
-  constexpr uint32_t rpb = threads / (D / 4), groups = R > rpb ? R / rpb : 1;
+  constexpr uint32_t groups = groups_of<D, R, threads>();
   hipLaunchKernelGGL((attention_join_kernel<kBf16, D, R, threads>), dim3(workers * groups), dim3(threads), 0, stream, p,
                      workers);
 }

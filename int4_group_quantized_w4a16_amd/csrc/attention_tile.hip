@@ -470,12 +470,12 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
     } else {
       float* const part = partial_of<R, D>(p, gridDim.x, 2 * walk.wg + (b0 == 0));
       if (mine) {
-        float* const row = part + (size_t)r * D + 4 * h;
+        float* const at = part + fragment_of<D>(r, 4 * h);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<floatx4*>(row + 32 * d + 8 * j) =
+            *reinterpret_cast<floatx4*>(at + (4 * d + j) * 256) =
                 floatx4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
         if (h == 0) {
           part[R * D + r] = m;
