@@ -18,7 +18,8 @@
 // * Measured with the join: 64 sequences of 125 to 8000 keys, 8 K/V heads of
 //   128 columns under 32, bf16: 182 us, 5.9 TB/s.  One sequence of 131000 keys:
 //   98 us, 5.5 TB/s.  Four of 225 to 900 keys, 32 heads, where launches and
-//   the latency of table, then keys, count: 18 us.
+//   the latency of table, then keys, count: 18 us.  Eight of 110 to 258 keys,
+//   in the direct form: 8.5 us.
 
 #include "attention_common.hpp"
 

@@ -45,10 +45,11 @@
 //   are added to the rows that see them afterwards, one by one.  Such blocks
 //   run in a loop of their own, so that the common one is small and keeps its
 //   accumulators in place.
-// * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 586 us, 938
-//   TFLOP/s.  1535 rows of three sequences over 4000 to 12000 cached keys, 32
-//   heads over 8: 247 us with the join (13), 819.  2049 rows of 16 heads of 64
-//   columns in a window of 4096: 70 us with the join (8), 490.  Of the first
+// * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 573 to 602 us by
+//   card, 587 = 937 TFLOP/s.  1535 rows of three sequences over 4000 to 12000
+//   cached keys, 32 heads over 8: 248 us with the join (13), 816.  2049 rows of
+//   16 heads of 64 columns in a window of 4096: 67 us with the join (8), 516.
+//   1024 causal tokens, 32 heads over 8: 28 us.  Of the first
 //   case's time 421 us remain without the softmax and 388 without the MFMAs
 //   (half of the cycles are the MFMAs' own): what bounds it is how far the two
 //   waves of a SIMD overlap.  Slower: 64 rows per wave with one wave per SIMD

@@ -9,7 +9,8 @@
 // Measured, weights from HBM: 8 x 4096 x 4096 with bias and residual 5.0 us
 // (a launch is 4); 61 x 11004 x 4096 with silu 14.2 us, bound by the latency of
 // one four-set tile per compute unit (22.5 MB of weights are 5 us); 2048 x 4096
-// x 4096 with everything 62.5 us, 1099 TFLOP/s, bound by MFMA.
+// x 4096 with everything 62.5 to 65 us by card, 1057 to 1099 TFLOP/s, bound by
+// MFMA.
 
 #include "w4a16_split_k.hpp"
 #include "w4a16_tile.hpp"
