@@ -250,7 +250,7 @@ struct AttentionPlan {
 // once.  A tile's block takes `alone` us with one workgroup on a compute unit, a split call `base` us more than a direct
 // one and `full` us per block and resident workgroup (the mean tile of a prompt has half of the last one's blocks).  us,
 // split / direct: 1024 tokens of 32 heads over 8, causal, 49 / 28; 4096 tokens 233 / 156; 1024 over 1024 58 / 46; 33 over
-// 2000 28 / 45; 300 over 1000 39 / 34 (split all the same); decode over 8 x 250 keys 12.8 / 8.5, 64 x 500 22.9 / 18.0,
+// 2000 25 / 45; 300 over 1000 36 / 34 (split all the same); decode over 8 x 250 keys 12.8 / 8.5, 64 x 500 22.9 / 18.0,
 // 16 x 900 15.2 / 21.4.  Past `most` blocks lengths that differ would leave too much to single workgroups.
 // If it holds for a number of blocks, it holds for fewer.
 constexpr bool attention_direct(bool stream, uint32_t head_dim, double blocks, double share, double mean) {
