@@ -369,6 +369,8 @@ class KaioPagedKV:
         _tensor(v_cache, "v_cache", (k_cache.dtype,), dev, rank=4, any_offset=True)
         if v_cache.shape != k_cache.shape:
             raise ValueError(f"v_cache must be {list(k_cache.shape)}, got {list(v_cache.shape)}")
+        if 0 in k_cache.shape[1:]:
+            raise ValueError(f"page_size, kv_heads and head_dim must be at least 1, got caches of {list(k_cache.shape)}")
         i32 = (torch.int32,)
         _tensor(page_table, "page_table", i32, dev, any_offset=True)
         _tensor(q_start, "q_start", i32, dev, rank=1, any_offset=True)

@@ -170,7 +170,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       return none();
     }
-    if (!kv || !fits(max_new) || !fits(window) || !fits(sinks)) return none();
+    if (!kv || kv->kv_heads == 0 || !fits(max_new) || !fits(window) || !fits(sinks)) return none();
     const at::Tensor* q = heads(a[0], *kv, dev);
     if (!q || q->size(1) % kv->kv_heads) return none();
     const uint32_t T = (uint32_t)q->size(0), hq = (uint32_t)q->size(1);

@@ -368,3 +368,14 @@ def test_a_window_needs_no_more_workspace():
     assert need > 0 and size(ctypes.byref(cache(table_width=4)), 3, 4, 1) == 0
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
     b.check(b.attention(workspace=ws))
+
+
+def test_a_cache_without_heads_goes_to_the_checks():
+    # the short call path must leave it to them (and not divide by its heads)
+    import ctypes
+    from tests.test_paged_host import paged as cache
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=DEV)
+    c = cache(kv_heads=0)
+    assert kaio._quick().attention(q, ctypes.addressof(c), q.device.index, 1, 1.0, 0, 0, None, None) is None
+    st = kaio.lib().kaio_paged_attention(ctypes.byref(c), q.data_ptr(), q.data_ptr(), 3, 4, 1, 1.0, 0, 0, None, 0, None)
+    assert st == 2 and "kv_heads" in kaio.kaio_last_error()      # INVALID_PROBLEM

@@ -168,3 +168,16 @@ def test_binding_refusals():
         kaio.kaio_paged_attention(torch.zeros(1, 2, 64, dtype=h), None, 1, 1.0)
     with pytest.raises(TypeError, match="float32"):
         kaio.KaioPagedKV(cpu.float(), cpu, i(1, 2), i(2), i(1))
+
+
+def test_caches_without_heads_columns_or_slots_per_page_are_refused(monkeypatch):
+    # nothing may divide by such a size later; a cache of no pages is a cache
+    import torch
+    monkeypatch.setattr(kaio, "_tensor", lambda t, *a, **k: t)     # (the checks of device and type are not at issue)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for shape in ((2, 0, 2, 64), (2, 16, 0, 64), (2, 16, 2, 0)):
+        cache = torch.zeros(shape, dtype=torch.float16)
+        with pytest.raises(ValueError, match="at least 1"):
+            kaio.KaioPagedKV(cache, cache.clone(), i(1, 2), i(2), i(1))
+    cache = torch.zeros(0, 16, 2, 64, dtype=torch.float16)
+    assert kaio.KaioPagedKV(cache, cache.clone(), i(1, 2), i(2), i(1)).pages == 0
