@@ -134,8 +134,9 @@ __device__ __forceinline__ u32x4 raw_rsrc(const char* base) {   // raw buffer, n
 // the builtin the compiler knows that LDS changes, cannot tell the buffers of a
 // ring apart, and waits for every load in flight before a read of any.  Callers
 // wait by wait_vm_barrier; the compiler's own counts for other loads only get
-// stricter by loads that it does not see.  The wait states cover m0 and a
-// descriptor that a lane read has just written.
+// stricter by loads that it does not see.  The wait states cover m0 (one) and a
+// descriptor that a lane read has just written (five); the compiler, which does
+// not see what the assembly reads, adds none.
 template <int kBytes>
 __device__ __forceinline__ void dma(const char* base, uint32_t off, void* lds) {
   const u32x4 rsrc = raw_rsrc(base);
@@ -146,13 +147,14 @@ __device__ __forceinline__ void dma(const char* base, uint32_t off, void* lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rsrc) : "m0");
 }
 // A K and a V load of the same cache rows: from the descriptors' bases + slot *
-// row_bytes (32 bits) + the lane's offsets to lds and lds + kApart.
+// row_bytes (32 bits) + the lane's offsets to lds and lds + kApart.  Five wait
+// states before the first load, as in dma; the second's descriptor has more.
 template <int kApart>
 __device__ __forceinline__ void dma16_pair(u32x4 krsrc, uint32_t koff, u32x4 vrsrc, uint32_t voff, uint32_t slot,
                                            uint32_t row_bytes, void* lds) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   uint32_t row;
-  asm volatile("s_mul_i32 %0, %1, %2\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %6, %0 offen lds\n\t"
+  asm volatile("s_mul_i32 %0, %1, %2\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dwordx4 %5, %6, %0 offen lds\n\t"
                "s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %7, %8, %0 offen lds"
                : "=&s"(row)
                : "s"(slot), "s"(row_bytes), "s"(at), "n"(kApart), "v"(koff), "s"(krsrc), "v"(voff), "s"(vrsrc)
