@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       }
       read_k(1 - kHalf, 0);
       bool special = false;
-      uint32_t there = 0;
+      uint32_t there = 0, sees = 0;
       if constexpr (kEdge) {
         const int32_t tile0 = key0_of(i) + 32 * kHalf;
         const int32_t mine = __shfl(sl0, (int)slot_lane(i, 32 * kHalf + l32));
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
         special = fix_v(b, there);
         // the keys of the tile that this lane's row sees, bit by bit: there, c <= pos, and c > floor or c < sinks
         auto first = [](int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };   // n ones
-        const uint32_t bits =
-            (there & first(pos - tile0 + 1) & (~first(floor - tile0 + 1) | first(sinks - tile0))) >> (4 * h);
+        sees = there & first(pos - tile0 + 1) & (~first(floor - tile0 + 1) | first(sinks - tile0));
+        const uint32_t bits = sees >> (4 * h);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           sc[e] = (int32_t)(bits << (31 - (8 * (e / 4) + e % 4))) < 0 ? sc[e] : -INFINITY;
@@ -396,18 +396,13 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (kEdge) {
         if (special) {
-          // the non-finite values of the tile, from the cache, to the rows that see their key
-          typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
-          const u32x8 wv = __builtin_bit_cast(u32x8, w);
+          // the non-finite values of the tile, from the cache, to the rows that see their key: as they are, since no
+          // weight changes them, also one that 16 bits round to zero
 #pragma unroll 1
-          for (int j = 0; j < 32; ++j) {            // key j: an element of half (j / 4) % 2
-            const int32_t s0 = __builtin_amdgcn_readlane(sl0, (int)slot_lane(i, 32 * kHalf + j));
-            const int32_t sj = (there >> j) & 1 ? s0 + (j & ((1 << ks) - 1)) : -1;
-            const int in_half = (j >> 2) & 1, e = 4 * (j >> 3) + (j & 3);
-            const uint32_t pair = wv[e >> 1];
-            const uint32_t pw = __shfl(e & 1 ? pair >> 16 : pair & 0xFFFFu, (int)l32 + 32 * in_half);
-            const float x = to_f32<kBf16>((uint16_t)pw);
-            if (sj < 0) continue;
+          for (int j = 0; j < 32; ++j) {
+            if (!((there >> j) & 1)) continue;
+            const int32_t sj = __builtin_amdgcn_readlane(sl0, (int)slot_lane(i, 32 * kHalf + j)) + (j & ((1 << ks) - 1));
+            const bool mine = (sees >> j) & 1;
             const uint16_t* const row = reinterpret_cast<const uint16_t*>(vhead + (size_t)sj * row_bytes) + 4 * h;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -417,7 +412,7 @@ __global__ void __launch_bounds__(256, 2) attention_tile_kernel(PagedAttention p
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                   const float vv = to_f32<kBf16>((uint16_t)(v[y >> 1] >> (16 * (y & 1))));
-                  o[d][4 * k + y] += x != 0.f && !(fabsf(vv) < INFINITY) ? x * vv : 0.f;
+                  o[d][4 * k + y] += mine && !(fabsf(vv) < INFINITY) ? vv : 0.f;
                 }
                 __builtin_amdgcn_sched_barrier(0);   // few registers at a time
               }

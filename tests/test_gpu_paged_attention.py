@@ -379,3 +379,27 @@ def test_a_cache_without_heads_goes_to_the_checks():
     assert kaio._quick().attention(q, ctypes.addressof(c), q.device.index, 1, 1.0, 0, 0, None, None) is None
     st = kaio.lib().kaio_paged_attention(ctypes.byref(c), q.data_ptr(), q.data_ptr(), 3, 4, 1, 1.0, 0, 0, None, 0, None)
     assert st == 2 and "kv_heads" in kaio.kaio_last_error()      # INVALID_PROBLEM
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("new,lens,extra", [([100, 3], [100, 90], 1), ([70, 40], [330, 61], 700), ([1, 2], [90, 61], 1)])
+def test_visible_non_finite_values_show_whatever_their_weight(new, lens, extra, bad, dtype, d):
+    # token 37's score is 60 under the others', a weight that 16 bits may round to zero, and one column of its V is not
+    # finite: every row that sees it must say so, no other row and no other column may
+    b = Batch(new, lens, 4, 2, d, 16, dtype, seed=25, extra_width=extra)
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k_cache.zero_()
+    b.scale = 1.0
+    for s in range(2):
+        at = b.table[s, 37 // 16], 37 % 16
+        b.k_cache[at][:, 0] = -60.0
+        b.v_cache[at][:, 5] = bad
+    out = f64(b.attention())
+    rows = paged.rows_of(b.q_start.numpy(), b.lens, b.tokens)
+    sees = np.array([pos >= 37 for _, pos in rows])
+    assert np.isfinite(out[~sees]).all() and np.isfinite(np.delete(out, 5, axis=2)).all()
+    hit = out[sees][:, :, 5]
+    assert np.isnan(hit).all() if np.isnan(bad) else not np.isfinite(hit).any()
