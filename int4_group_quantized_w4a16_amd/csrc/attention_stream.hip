@@ -12,6 +12,10 @@
 //   l16) holds row l16's keys 4 kb + (0..3) of each, which are, in this order,
 //   its B operand of O^T = V^T.P^T over the 32 keys; V^T by transposed LDS
 //   reads.
+// * Softmax as in the tile form: f32 scores, maxima and sums, weights rounded
+//   to the 16-bit type for the second product (f32 weights would take it out of
+//   the 16-bit MFMAs), and their sum taken of the rounded ones, so that the
+//   weights used add up to one.
 // * Each wave's next 16 KiB of K and V are in flight in registers while the
 //   current ones are computed on: 128 KiB per CU, four times what the memory
 //   latency needs.  Both as non-temporal loads: a cache is read once per step.
@@ -195,9 +199,8 @@ __global__ void __launch_bounds__(256, 2) attention_stream_kernel(PagedAttention
         for (int e = 0; e < 8; e += 2) {
           const float a = exp2_fast(__builtin_fmaf(s[e >> 2][e & 3], c, base));
           const float b = exp2_fast(__builtin_fmaf(s[e >> 2][(e & 3) + 1], c, base));
-          l += a;
-          l += b;
           pk[e / 2] = pack2<kBf16>(a, b);
+          l = add2<kBf16>(pk[e / 2], l);
         }
         const short8_t w = __builtin_bit_cast(short8_t, pk);
         const uint32_t vrow = 4 * kb + (l16 >> 2);

@@ -403,3 +403,25 @@ def test_visible_non_finite_values_show_whatever_their_weight(new, lens, extra, 
     assert np.isfinite(out[~sees]).all() and np.isfinite(np.delete(out, 5, axis=2)).all()
     hit = out[sees][:, :, 5]
     assert np.isnan(hit).all() if np.isnan(bad) else not np.isfinite(hit).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("length,extra", [(64, 1), (1500, 700)])
+def test_the_weights_used_add_up_to_one(length, extra, new, dtype, d):
+    # weights a little under half a step of the 16-bit type above a power of two, all rounded the same way, and V = 1:
+    # the weights that multiply V are those that are summed, so the result is 1 but for 2 n f32 roundings, which is 1
+    # in 16 bits (2 * 1500 * 2^-24 is under 2^-12, half a step under 1 of f16)
+    b = Batch([new], [length], 2, 1, d, 16, dtype, seed=26, extra_width=extra)
+    b.q.zero_()
+    b.q[:, :, :2] = 1.0
+    b.k_cache.zero_()
+    b.k_cache[..., 0] = -3.0
+    b.k_cache[..., 1] = float(np.log2(1 + 0.9 * 2.0 ** (-11 if dtype == "f16" else -8)))
+    for t in range(0, length, 32):                      # a key of weight 1 in whatever part of the keys has its own maximum
+        b.k_cache[b.table[0, t // 16], t % 16, :, :2] = 0.0
+    b.v_cache.fill_(1.0)
+    b.scale = float(np.log(2.0))
+    out = b.attention()
+    assert torch.equal(out, torch.ones_like(out))
