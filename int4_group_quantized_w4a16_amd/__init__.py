@@ -99,15 +99,23 @@ _fast = None
 
 def _quick():
     """csrc/torch_binding.cpp, bound to the loaded library: the short way of ordinary calls.  It returns None for
-    anything it does not take, which then goes through the checks below.  False where it was never built."""
+    anything it does not take, which then goes through the checks below.  False where it was never built, or was built
+    for another torch than the one that is loaded."""
     global _fast
     if _fast is None:
         L = lib()
-        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")):
-            _fast = False
-        else:
-            import torch  # noqa: F401  (its libraries come first)
-            from . import _binding as b
+        _fast = False
+        if os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")):
+            import warnings
+            import torch  # (its libraries come first)
+            try:
+                from . import _binding as b
+            except ImportError as e:
+                warnings.warn(f"_binding.so does not load, calls go through ctypes: {e}")
+                return _fast
+            if getattr(b, "torch_version", None) != torch.__version__:
+                warnings.warn("_binding.so was built for another torch, calls go through ctypes: build again")
+                return _fast
             b.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.kaio_linear_w4a16, L.kaio_rope_append, L.kaio_paged_attention, L.kaio_paged_attention_workspace_size)])
             _fast = b

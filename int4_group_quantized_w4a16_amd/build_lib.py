@@ -20,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -102,7 +103,7 @@ def build_host_sanitized(verbose: bool = False) -> str:
 
 
 def build_binding() -> str:
-    """_binding.so: csrc/torch_binding.cpp by the host compiler."""
+    """_binding.so: csrc/torch_binding.cpp by the host compiler, for the torch that is here (it says which)."""
     import sysconfig
 
     import torch
@@ -112,7 +113,8 @@ def build_binding() -> str:
     libs = os.path.join(root, "lib")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DKAIO_TORCH_VERSION="{torch.__version__}"', *[f"-I{i}" for i in inc],
            os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
            "-lc10_hip", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -122,19 +124,32 @@ def build_binding() -> str:
     return BINDING
 
 
+def _binding_if_possible() -> str:
+    """build_binding(), or, where torch's headers, its libraries or a host compiler are missing, a warning and no
+    binding (nor an older one): Python then calls the C library by ctypes, a few us slower per call."""
+    try:
+        return build_binding()
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        warnings.warn(f"{os.path.basename(BINDING)} was not built, calls go through ctypes: {e}")
+        return ""
+
+
 def build(extra_flags=(), verbose: bool = False) -> str:
     """Compile every source for gfx950, link libkaio.so (and the benchmark's
-    libkaio_roof.so) and the Python binding; returns the path of libkaio.so."""
+    libkaio_roof.so) and, where that is possible, the Python binding; returns the
+    path of libkaio.so."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = SOURCES + ROOF_SOURCES
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        binding = ex.submit(build_binding)
+        binding = ex.submit(_binding_if_possible)
         objs = list(ex.map(lambda s: _compile(s, list(extra_flags)), srcs))
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], ROOF_LIB)
-    binding.result()
+    built = [LIB, ROOF_LIB] + [b for b in (binding.result(),) if b]
     if verbose:
-        print(f"built {LIB}, {ROOF_LIB} and {BINDING}")
+        print("built " + ", ".join(built))
     return LIB
 
 

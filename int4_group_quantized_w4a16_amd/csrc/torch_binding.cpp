@@ -225,4 +225,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose headers this was compiled with: tensors of another one need not be laid out alike
+  if (m && PyModule_AddStringConstant(m, "torch_version", KAIO_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
