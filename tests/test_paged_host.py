@@ -181,3 +181,49 @@ def test_caches_without_heads_columns_or_slots_per_page_are_refused(monkeypatch)
             kaio.KaioPagedKV(cache, cache.clone(), i(1, 2), i(2), i(1))
     cache = torch.zeros(0, 16, 2, 64, dtype=torch.float16)
     assert kaio.KaioPagedKV(cache, cache.clone(), i(1, 2), i(2), i(1)).pages == 0
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(tokens=600, max_new=600), dict(tokens=600, max_new=600, window=1000, sinks=4),
+                                dict(head_dim=128, kv_heads=4, dtype=BF16)])
+def test_workspace_refusals_of_calls_that_split_their_keys(kw):
+    kw = dict(kw, table_width=300)                              # room for 4800 tokens: keys are split and joined
+    need = kaio.lib().kaio_paged_attention_workspace_size(
+        ctypes.byref(paged(**{k: v for k, v in kw.items() if k not in ("tokens", "max_new", "window", "sinks")})),
+        kw.get("tokens", 3), 4, kw.get("max_new", 1))
+    assert need > 0
+    for change, msg in ((dict(ws=0, ws_bytes=need), "workspace is null"), (dict(ws=0, ws_bytes=0), "workspace is null"),
+                        (dict(ws_bytes=need - 1), f"workspace_bytes ({need - 1}) < {need} needed"),
+                        (dict(ws_bytes=0), "workspace_bytes (0)"),
+                        (dict(ws=A + 7 * STEP + 4), "workspace is not 16-byte aligned"),
+                        (dict(ws=A + 5 * STEP + 16), "workspace overlaps q"),
+                        (dict(ws=A + 6 * STEP + 16), "out overlaps workspace"),
+                        (dict(ws=A + 16), "workspace overlaps k_cache"), (dict(ws=A + STEP + 16), "workspace overlaps v_cache"),
+                        (dict(ws=A + 2 * STEP + 16), "workspace overlaps page_table"),
+                        (dict(ws=A + 3 * STEP), "workspace overlaps q_start"), (dict(ws=A + 4 * STEP), "workspace overlaps lens")):
+        st, text = attn(**kw, **change)
+        assert st == ARG and msg in text, (change, text)
+
+
+@no_gpu_only
+def test_workspace_of_calls_that_split_and_calls_that_do_not():
+    c = paged(table_width=4)
+    assert kaio.lib().kaio_paged_attention_workspace_size(ctypes.byref(c), 3, 4, 1) == 0
+    assert attn(ws=0, ws_bytes=0)[0] == DEVICE                  # no workspace where none is needed
+    assert attn(ws=A + 5 * STEP + 4, ws_bytes=0)[0] == DEVICE   # nor are one's address and size looked at
+    assert attn(table_width=300)[0] == DEVICE                   # exactly what the query says is enough
+    need = kaio.lib().kaio_paged_attention_workspace_size(ctypes.byref(paged(table_width=300)), 3, 4, 1)
+    assert attn(table_width=300, ws_bytes=2 * need)[0] == DEVICE
+
+
+def test_a_window_asks_for_no_more_workspace_than_the_query_says():
+    # over many sizes: a call with a window that is refused for its null workspace is one whose query was not 0
+    for seqs, tokens, max_new in ((1, 1, 1), (3, 3, 1), (64, 64, 1), (300, 300, 1), (1, 700, 700), (5, 2000, 900), (40, 400, 10)):
+        for width in (1, 10, 100, 1000, 20000):
+            for window, sinks in ((1, 0), (64, 4), (1000, 0), (5000, 70), (2 ** 31, 2 ** 31), (2 ** 32 - 1, 2 ** 32 - 1)):
+                for d, hkv, hq in ((64, 1, 8), (128, 8, 8), (128, 2, 32)):
+                    kw = dict(seqs=seqs, tokens=tokens, max_new=max_new, table_width=width, head_dim=d, kv_heads=hkv, hq=hq)
+                    need = kaio.lib().kaio_paged_attention_workspace_size(
+                        ctypes.byref(paged(seqs=seqs, table_width=width, head_dim=d, kv_heads=hkv)), tokens, hq, max_new)
+                    # out = q: the next check after the workspace's size refuses it, on the host
+                    st, text = attn(out=A + 5 * STEP, window=window, sinks=sinks, ws=A + 8 * STEP, ws_bytes=need, **kw)
+                    assert st == ARG and "out overlaps q" in text, (kw, window, sinks, need, text)
