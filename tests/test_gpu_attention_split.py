@@ -275,3 +275,27 @@ def test_graph_replays_and_used_workspaces(new, window, sinks):
         eager = kaio.kaio_paged_attention(b.dq, b.paged, max(new), b.scale, window=window, sinks=sinks)
         torch.cuda.synchronize()
         assert torch.equal(eager, out)
+
+
+def test_as_many_sequences_as_the_schedule_holds():
+    # 512 tiles, most of sequences without new tokens
+    new = [1 if i in (0, 3, 64, 65, 300, 510, 511) else 0 for i in range(512)]
+    lens = [1200 if i == 65 else 90 if n else i % 3 for i, n in enumerate(new)]
+    b = Batch(new, lens, 2, 2, 64, 16, "f16", seed=30, pad=2, extra_width=wide(16))
+    b.check(attention(b))
+
+
+@pytest.mark.parametrize("extra", [1, wide(16)])
+@pytest.mark.parametrize("d", [64, 128, 80])
+@pytest.mark.parametrize("new", [[1, 1], [50, 3]])
+def test_rows_before_the_first_sequence(new, d, extra):
+    # q_start need not begin at 0: rows before it see nothing, whole tables or wide ones, whatever the form
+    lead = 5
+    b = Batch(new, [300, 77], 4, 2, d, 16, "f16", seed=31, pad=lead + 3, extra_width=extra)
+    b.q_start += lead
+    b.on_gpu()
+    assert splits(b) == (extra > 1 and d != 80)
+    out = b.attention()
+    b.check(out)
+    y = f64(out)
+    assert not y[:lead].any() and not y[-3:].any() and y[lead:-3].any()

@@ -6,6 +6,7 @@ import torch
 import int4_group_quantized_w4a16_amd as kaio
 from oracle import linear as ol
 from tests.gpu_util import DEV, to_dev, to_host
+from tests.linear_forms import SIZES
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +120,8 @@ def test_repeats_streams_and_graphs():
             torch.cuda.synchronize()
             got = out.clone()
             assert torch.equal(got, kaio.kaio_linear_w4a16(x, w, s, bias=b, activation="silu", residual=res))
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_every_form(m, n, k):
+    run_case(m, n, k, "gelu_tanh", seed=7)
