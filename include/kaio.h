@@ -1,20 +1,21 @@
 /*
  * kaio.h -- C ABI of the MI355X (gfx950) W4A16 fused-QKV library.
  *
- * Each operation is one asynchronous launch on the caller's HIP stream:
+ * Each operation is asynchronous on the caller's HIP stream, one launch unless
+ * noted:
  *
  *   kaio_qkv_w4a16          W4A16 group-quantized fused tri-output QKV projection
  *   kaio_qkv_w8a16          its W8A16 sibling (INT8 weights, same contract)
  *                           (kaio_qkv_plan: which kernel form a call of given sizes runs)
  *   kaio_gemm_f16f32        dense f16 x f16 -> f32 matmul
- *   kaio_gemm_f16f32_bwd    its backward: f16 gradients of A and B
+ *   kaio_gemm_f16f32_bwd    its backward: f16 gradients of A and B (three launches)
  *                           (kaio_gemm_f16f32_bwd_noalloc: the same without a workspace)
  *   kaio_dequant_group_bwd  straight-through per-group dequant backward
  *   kaio_linear_w4a16       W4A16 product with bias, activation and residual
  *   kaio_rope_append        rotary positions on Q and K, K and V written to a
  *                           paged cache
- *   kaio_paged_attention    attention of new tokens over that cache (with a
- *                           second launch where the keys of a row are split)
+ *   kaio_paged_attention    attention of new tokens over that cache (two
+ *                           launches where the keys of a row are split)
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -352,10 +353,26 @@ kaio_status kaio_rope_append(const kaio_paged_kv* kv, const void* q, const void*
  *
  * over the visible positions c of the row at position pos: c <= pos, c <
  * lens[s], its page there, and, with window > 0, c > pos - window or c < sinks.
- * A row that sees nothing is zero.  Scores, softmax and sums are f32.
- * Invisible positions are not read into the result, whatever they hold.
- * Scores of a magnitude past 2^26, where f32's steps exceed the weights'
- * range, may make their row NaN.
+ * A row that sees nothing is zero.  Scores, maxima, sums and the output's
+ * accumulation are f32.  The weights are rounded to the cache's type for the
+ * product with V at head_dim 64 and 128 (half a step each; the sum is taken of
+ * the rounded ones), and stay f32 at other sizes.  Invisible positions are not
+ * read into the result, whatever they hold; a visible value that is not finite
+ * shows in the result however small its weight.  Scores of a magnitude past 2^26,
+ * where f32's steps exceed the weights' range, may make their row NaN.
+ *
+ * Speed follows from what the host knows, the lengths not among it: a table
+ * not much wider than the sequences need lets short calls run in one launch,
+ * one workgroup per tile, where a wide one splits the keys and joins the
+ * pieces (512 / 1024 / 4096 new tokens of 32 heads over 8, 128 columns: 18 / 30
+ * / 160 us against 32 / 47 / 231 us with room for 131072 tokens).  Keys are
+ * never split in calls of many tiles, and one long sequence among short ones
+ * then takes its own time: a tile is 128 rows (tokens times heads of a group),
+ * or 16 where max_new * group is at most 16, every sequence counts one more,
+ * and many are more than 512, or 2048 and more over all K/V heads.  With tiles
+ * of 128 rows a cache tensor past 4 GiB, or a page_size that is no multiple of
+ * 4 (128 columns) or 8 (64), costs 1.4 times the time.  Head sizes other than
+ * 64 and 128 run a simple kernel, tens of times slower.
  *
  *   q, out  [tokens, q_heads, head_dim]
  *   max_new    the most new tokens a sequence has (it chooses the kernel; a

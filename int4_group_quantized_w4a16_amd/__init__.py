@@ -366,6 +366,9 @@ class KaioPagedKV:
     q_start           int32 [seqs + 1], ascending: rows of q of each sequence's new tokens
     lens              int32 [seqs]: tokens of each sequence, the new ones last
 
+    The host does not know the lengths, so ``width`` decides how attention shares out its work: short prompts and short
+    caches are faster with a table not much wider than its sequences need (include/kaio.h has figures).
+
     Holds the tensors; made once and kept while they live, as only their addresses and shapes are taken here.
     What page_table, q_start and lens hold is read on the device by each call.
     """

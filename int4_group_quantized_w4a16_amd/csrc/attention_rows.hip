@@ -6,7 +6,12 @@
 // over the visible positions c of the row at position pos: 0 <= c <= pos, the
 // page there, and with a window c > pos - window or c < sinks.  A row that sees
 // nothing is zero.  Lane j scores key 64 b + j of block b; the running maximum
-// and sum go with the blocks, so each key is read once.
+// and sum go with the blocks, so each key is read once per row and head.
+//
+// A simple kernel, bound by its loads' latency: each lane walks its key by
+// 2-byte loads, and the wave V key by key.  64 sequences of 125 to 8000 keys,
+// bf16: 32 heads over 8 of 80 or 96 columns 6.2 ms, 16 over 4 of 256 13.4 ms
+// (0.1 TB/s); 512 causal tokens, 32 heads over 8 of 96: 344 us.
 
 #include "launch.hpp"
 #include "paged.hpp"

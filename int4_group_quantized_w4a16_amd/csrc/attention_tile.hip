@@ -22,9 +22,12 @@
 //   from transposed LDS reads of four keys each in the same order.
 // * The cache rows of a tile go straight to LDS (direct loads) three tiles
 //   ahead; one barrier per tile.  Lane j of each wave looks up the slot of key
-//   j of a block, a block ahead of that.  A load covers 4 (64 columns: 8) keys; where they share a page (page_size a multiple of
-//   that) it takes a wave-uniform 64-bit base and one lane offset, otherwise
-//   one load per key.
+//   j of a block, a block ahead of that.  A load covers 4 (64 columns: 8)
+//   keys.  Where they share a page (page_size a multiple of that) and the cache
+//   is below 4 GiB per tensor, it takes the slot as a 32-bit scalar offset from
+//   the head's base; otherwise there is a load, with a 64-bit base, per key
+//   (1535 rows over 4000 to 12000 keys, as below: 351 us in a cache of 5 GiB,
+//   342 with pages of 6, 246 so).
 // * LDS rows are unpadded (a direct load writes lane-contiguous chunks), so
 //   bank conflicts are avoided by where each 16-byte chunk is put: K chunk c
 //   of row r at c ^ (r % 16), V at its 64-byte window xor r % 4 (64 columns:
@@ -42,14 +45,17 @@
 //   bits of a word (comparing key by key: 75.8 us for the windowed case below,
 //   69.1 so).  In those blocks a pass over V in LDS zeroes slots that are not
 //   there and non-finite values (weight 0 times infinity is not 0); the latter
-//   are added to the rows that see them afterwards, one by one.  Such blocks
+//   are added to the rows that see them afterwards, as they are.  Such blocks
 //   run in a loop of their own, so that the common one is small and keeps its
 //   accumulators in place.
-// * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 573 to 602 us by
-//   card, 587 = 937 TFLOP/s.  1535 rows of three sequences over 4000 to 12000
-//   cached keys, 32 heads over 8: 248 us with the join (13), 816.  2049 rows of
-//   16 heads of 64 columns in a window of 4096: 67 us with the join (8), 516.
-//   1024 causal tokens, 32 heads over 8: 28 us.  Of the first
+// * Measured: 8192 causal keys, 32 heads of 128 columns, f16: 571 to 616 us by
+//   card, 578 = 952 TFLOP/s.  1535 rows of three sequences over 4000 to 12000
+//   cached keys, 32 heads over 8: 244 us with the join (13), 828.  2049 rows of
+//   16 heads of 64 columns in a window of 4096: 66 us with the join (8), 525.
+//   1024 causal tokens, 32 heads over 8: 28 to 30 us.  MFMA and vector unit
+//   busy: 54% and 51% of the first case's cycles, 53% and 48%, 30% and 52%; the
+//   waves wait 38%, 37%, 30% of their cycles to issue and 20%, 22%, 26% for
+//   loads and barriers.  Of the first
 //   case's time 421 us remain without the softmax and 388 without the MFMAs
 //   (half of the cycles are the MFMAs' own): what bounds it is how far the two
 //   waves of a SIMD overlap.  Slower: 64 rows per wave with one wave per SIMD

@@ -249,9 +249,11 @@ struct AttentionPlan {
 // no schedule to derive and nothing to join.  blocks: a bound on a tile's; share: tiles over workgroups resident at
 // once.  A tile's block takes `alone` us with one workgroup on a compute unit, a split call `base` us more than a direct
 // one and `full` us per block and resident workgroup (the mean tile of a prompt has half of the last one's blocks).  us,
-// split / direct: 1024 tokens of 32 heads over 8, causal, 49 / 28; 4096 tokens 233 / 156; 1024 over 1024 58 / 46; 33 over
-// 2000 25 / 45; 300 over 1000 36 / 34 (split all the same); decode over 8 x 250 keys 12.8 / 8.5, 64 x 500 22.9 / 18.0,
-// 16 x 900 15.2 / 21.4.  Past `most` blocks lengths that differ would leave too much to single workgroups.
+// split / direct: 1024 tokens of 32 heads over 8, causal, 49 / 28; 4096 tokens 231 / 156; 1024 over 1024 58 / 46; 33 over
+// 2000 25 / 45; 300 over 1000 36 / 34 (split all the same, by the rule); decode over 8 x 250 keys 12.8 / 8.5, 64 x 500
+// 22.9 / 18.0, 16 x 900 15.2 / 21.4.  Past `most` blocks lengths that differ could leave too much to single workgroups.
+// The limit holds for one sequence too, whose tiles differ only by their place in it: 4160 / 6144 / 8000 tokens, split,
+// take 230 / 453 / 664 us, 4096 and 8192 (by the number of tiles), direct, 160 and 555.
 // If it holds for a number of blocks, it holds for fewer.
 constexpr bool attention_direct(bool stream, uint32_t head_dim, double blocks, double share, double mean) {
   const double alone = stream ? 2.0 : head_dim == 128 ? 1.24 : 0.85, full = stream ? 2.0 : head_dim == 128 ? 2.5 : 1.7;

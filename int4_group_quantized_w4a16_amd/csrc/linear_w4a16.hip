@@ -7,10 +7,12 @@
 // sums kept in f32 through the epilogue and rounded once.
 //
 // Measured, weights from HBM: 8 x 4096 x 4096 with bias and residual 5.0 us
-// (a launch is 4); 61 x 11004 x 4096 with silu 14.2 us, bound by the latency of
-// one four-set tile per compute unit (22.5 MB of weights are 5 us); 2048 x 4096
-// x 4096 with everything 62.5 to 65 us by card, 1057 to 1099 TFLOP/s, bound by
-// MFMA.
+// (a launch is 4); 61 x 11004 x 4096 with silu 14.2 us (22.5 MB of weights are 5
+// us): 172 tiles leave 84 compute units idle, and on the others no unit is the
+// bound (vector unit 45% busy, LDS 34%, MFMA 27%): the waves wait 43% of their
+// cycles for loads and barriers, one four-set tile per compute unit; 2048 x 4096
+// x 4096 with everything 62.5 to 65 us by card, 1057 to 1099 TFLOP/s, MFMA and
+// vector unit 51% and 52% busy.
 
 #include "w4a16_split_k.hpp"
 #include "w4a16_tile.hpp"

@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeAppend p, uin
   }
 }
 
-// Element form for the other sizes: one thread per pair or pass-through element.
+// Element form for the other sizes: one thread per pair or pass-through element,
+// 2-byte accesses (16384 tokens, 32 + 2 x 8 heads of 80 columns: 175 us with 20
+// pairs, against 52 us of the vector form with 40; 4 tokens, 96 heads of 72: 11).
 template <bool kBf16, bool kInter>
 __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(RopeAppend p) {
   extern __shared__ float cs[];
