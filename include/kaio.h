@@ -12,6 +12,12 @@
  *                           (kaio_gemm_f16f32_bwd_noalloc: the same without a workspace)
  *   kaio_dequant_group_bwd  straight-through per-group dequant backward
  *   kaio_linear_w4a16       W4A16 product with bias, activation and residual
+ *   kaio_quantize_rows      rows of 16-bit numbers rounded to 8 bits
+ *   kaio_linear_w8a8        product in 8-bit integers with scales for each
+ *                           token and channel, and the same epilogue (two
+ *                           launches where it rounds x)
+ *   kaio_moe_w4a16          mixture-of-experts feed-forward on W4A16 weights
+ *                           (four launches)
  *   kaio_rope_append        rotary positions on Q and K, K and V written to a
  *                           paged cache
  *   kaio_paged_attention    attention of new tokens over that cache (two
@@ -285,6 +291,122 @@ kaio_status kaio_linear_w4a16(const void* x, const uint32_t* w, const void* s,
                               const void* bias, const void* residual, void* y,
                               uint32_t m, uint32_t n, uint32_t k, uint32_t group_size,
                               kaio_activation activation, void* stream);
+
+/*
+ * Rows rounded to 8 bits, each with a scale of its own:
+ *
+ *   a[i] = max_j |x[i, j]|     scale[i] = a[i] / 127
+ *   q[i, j] = round(127 x[i, j] / a[i])          (ties to even)
+ *
+ * exactly: q is the formula's integer, scale the nearest f32.  A row of zeros
+ * has scale 0 and q 0; a row with an infinity or a NaN has scale NaN and q 0,
+ * so that what is computed of it is NaN.
+ *
+ *   x  f16 or bf16 [m, k] (dtype)     q  int8[m, k]     scale  f32[m]
+ *
+ * Validation order: dtype not f16 or bf16 -> UNSUPPORTED; k % 16 != 0 ->
+ * INVALID_PROBLEM; m == 0 -> OK (nothing launched); too large (m >= 2^24,
+ * k >= 2^24) -> INVALID_PROBLEM; null pointer (x and q only when k > 0) ->
+ * INVALID_ARGUMENT; misaligned (16 bytes) -> INVALID_ARGUMENT; overlapping ->
+ * INVALID_ARGUMENT; device -> DEVICE; launch -> LAUNCH.
+ */
+kaio_status kaio_quantize_rows(kaio_dtype dtype, const void* x, int8_t* q, float* scale,
+                               uint32_t m, uint32_t k, void* stream);
+
+/*
+ * Product in 8-bit integers with a scale for each token and each channel:
+ *
+ *   y[i, j] = act( xs[i] * ws[j] * sum_k xq[i, k] * w[j, k] + b[j] ) + r[i, j]
+ *
+ *   dtype     KAIO_DTYPE_F16 or KAIO_DTYPE_BF16: y, bias and residual, and x where
+ *             it is rounded here
+ *   x         with x_scale: int8[m, k], and x_scale f32[m].
+ *             x_scale NULL: [m, k] in dtype, rounded as by kaio_quantize_rows
+ *             (the results are those of the two calls, bit for bit)
+ *   w         int8[n, k] (a row per output channel)     w_scale  f32[n]
+ *   bias      [n] or NULL          residual  [m, n] or NULL
+ *   y         [m, n]; may be the residual's buffer itself (updated in place)
+ *   workspace device scratch of at least kaio_linear_w8a8_workspace_size bytes,
+ *             16-byte aligned (NULL when that is 0); unspecified on return.
+ *             Calls on one workspace must not overlap in time.
+ *
+ * The sum is exact, in i32; scales, bias, activation and residual are in f32,
+ * rounded once to dtype (RNE).
+ *
+ * Validation order: dtype -> UNSUPPORTED; unknown activation -> UNSUPPORTED;
+ * k % 16 != 0, k > 131056 -> INVALID_PROBLEM; m == 0 or n == 0 -> OK (nothing
+ * launched); too large for one launch (m >= 2^24, n >= 2^26, 2^24 - 1
+ * workgroups) -> INVALID_PROBLEM; null pointer (x and w only when k > 0),
+ * workspace too small, misaligned pointer (16 bytes), y or the workspace
+ * overlapping an input (other than residual == y) -> INVALID_ARGUMENT; device
+ * -> DEVICE; launch -> LAUNCH.  k == 0: the product is zero, the epilogue
+ * still runs.
+ */
+kaio_status kaio_linear_w8a8(kaio_dtype dtype, const void* x, const float* x_scale, const int8_t* w,
+                             const float* w_scale, const void* bias, const void* residual, void* y,
+                             uint32_t m, uint32_t n, uint32_t k, kaio_activation activation,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes kaio_linear_w8a8 needs for these sizes (0 for sizes it refuses); int8_x: x_scale is given. */
+size_t kaio_linear_w8a8_workspace_size(uint32_t m, uint32_t n, uint32_t k, int32_t int8_x);
+
+/*
+ * The weights of a mixture-of-experts feed-forward.  The struct itself is in
+ * host memory and read during the call; the pointers are device pointers.
+ * Packed weights and scales as kaio_linear_w4a16's, one after the other.
+ */
+typedef struct kaio_experts {
+  const void* router;      /* f16[experts, hidden]                     */
+  const uint32_t* w_gate;  /* u32[experts, hidden / 8, inner]          */
+  const void* s_gate;      /* f16[experts, hidden / 128, inner]        */
+  const uint32_t* w_up;    /* as w_gate                                */
+  const void* s_up;        /* as s_gate                                */
+  const uint32_t* w_down;  /* u32[experts, inner / 8, hidden]          */
+  const void* s_down;      /* f16[experts, inner / 128, hidden]        */
+  uint32_t experts, hidden, inner;
+  uint32_t group_size;     /* must be 128                              */
+} kaio_experts;
+
+/*
+ * A whole mixture-of-experts feed-forward for a few tokens:
+ *
+ *   z[t, e] = sum_h x[t, h] * router[e, h]
+ *   E(t)    = the top_k experts of largest z[t, e] (ties: the lowest e)
+ *   p[t, e] = exp(z[t, e]) / sum exp(z[t, .]), the sum over E(t) with
+ *             normalize, else over all experts
+ *   h[t, e] = act(x[t] . Wgate[e]) * (x[t] . Wup[e])            f16[inner]
+ *   y[t]    = sum over E(t) of p[t, e] * (h[t, e] . Wdown[e])  + r[t]
+ *
+ *   x  f16[tokens, hidden]     residual  the same shape, or NULL
+ *   y  f16[tokens, hidden]; may be the residual's buffer itself
+ *   workspace  device scratch of at least kaio_moe_w4a16_workspace_size bytes,
+ *              16-byte aligned; unspecified on return.  Calls on one workspace
+ *              must not overlap in time.
+ *
+ * z is summed in f64, so experts come in the order of the formula.  A score
+ * that is NaN comes after every number.  Products are accumulated in f32, h is
+ * rounded to f16 (half a step; past 65504 it is infinite, as any f16
+ * activation), y is rounded once.  A token sees its own experts only, whatever
+ * the others hold.  Results are the same on every run.
+ *
+ * Made for few tokens: the chosen experts' weights are read once for each 64
+ * tokens.  More are computed as rightly, 64 at a time.
+ *
+ * Validation order: e null -> INVALID_ARGUMENT; group_size, activation, experts
+ * > 512 or top_k > 16 -> UNSUPPORTED; hidden or inner zero or no multiple of
+ * 128, top_k not in [1, experts] -> INVALID_PROBLEM; tokens == 0 -> OK (nothing
+ * launched); too large (tokens > 2^17, hidden or inner >= 2^24, 2^24 - 1
+ * workgroups) -> INVALID_PROBLEM; null pointer, workspace too small, misaligned
+ * pointer (16 bytes), y or the workspace overlapping an input (other than
+ * residual == y) -> INVALID_ARGUMENT; device -> DEVICE; launch -> LAUNCH.
+ */
+kaio_status kaio_moe_w4a16(const kaio_experts* e, const void* x, const void* residual, void* y,
+                           uint32_t tokens, uint32_t top_k, int32_t normalize,
+                           kaio_activation activation, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace bytes kaio_moe_w4a16 needs for these sizes (0 for sizes it refuses). */
+size_t kaio_moe_w4a16_workspace_size(const kaio_experts* e, uint32_t tokens, uint32_t top_k);
 
 /*
  * A paged key/value cache and the batch that uses it.  The struct itself is in

@@ -12,6 +12,10 @@ device is not gfx950 the call raises.
     kaio_gemm_f16f32_bwd(a, b, grad) -> (grad_a, grad_b)
     kaio_dequant_group_bwd(dy, scale, group_size) -> dq
     kaio_linear_w4a16(x, w, s, bias=, activation=, residual=) -> y
+    kaio_quantize_rows(x) -> (q, scale)
+    kaio_linear_w8a8(x, w, w_scale, x_scale=, bias=, activation=, residual=) -> y
+    KaioExperts(router, w_gate, s_gate, w_up, s_up, w_down, s_down): the weights of a mixture of experts, for
+    kaio_moe_w4a16(x, experts, top_k, normalize=, activation=, residual=) -> y
     KaioPagedKV(k_cache, v_cache, page_table, q_start, lens): a paged cache and its batch, for
     kaio_rope_append(q, k, v, positions, inv_freq, sections, paged) -> q
     kaio_paged_attention(q, paged, max_new, scale, window=, sinks=) -> out
@@ -22,7 +26,8 @@ import ctypes
 import os
 
 __all__ = ["DTYPE_CODES", "KaioError", "kaio_qkv_w4a16", "kaio_qkv_w8a16", "kaio_gemm_f16f32", "kaio_gemm_f16f32_bwd",
-           "kaio_dequant_group_bwd", "kaio_linear_w4a16", "KaioPagedKV", "kaio_rope_append", "kaio_paged_attention",
+           "kaio_dequant_group_bwd", "kaio_linear_w4a16", "kaio_quantize_rows",
+           "kaio_linear_w8a8", "KaioExperts", "kaio_moe_w4a16", "KaioPagedKV", "kaio_rope_append", "kaio_paged_attention",
            "ACTIVATION_CODES",
            "kaio_last_error", "kaio_version", "lib", "LIB_PATH", "GROUP_SIZE"]
 
@@ -53,6 +58,12 @@ class _PagedKV(ctypes.Structure):
                [(n, ctypes.c_uint32) for n in ("pages", "page_size", "kv_heads", "head_dim", "seqs", "table_width")]
 
 
+class _Experts(ctypes.Structure):
+    """kaio_experts of include/kaio.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("router", "w_gate", "s_gate", "w_up", "s_up", "w_down", "s_down")] + \
+               [(n, ctypes.c_uint32) for n in ("experts", "hidden", "inner", "group_size")]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded C library (loads on first use; raises if it was never built)."""
     global _lib
@@ -80,6 +91,16 @@ def lib() -> ctypes.CDLL:
         L.kaio_qkv_plan.restype = ctypes.c_int
         L.kaio_linear_w4a16.argtypes = [vp] * 6 + [u32] * 4 + [ctypes.c_int, vp]
         L.kaio_linear_w4a16.restype = ctypes.c_int
+        L.kaio_quantize_rows.argtypes = [ctypes.c_int] + [vp] * 3 + [u32] * 2 + [vp]
+        L.kaio_quantize_rows.restype = ctypes.c_int
+        L.kaio_linear_w8a8.argtypes = [ctypes.c_int] + [vp] * 7 + [u32] * 3 + [ctypes.c_int, vp, ctypes.c_size_t, vp]
+        L.kaio_linear_w8a8.restype = ctypes.c_int
+        L.kaio_linear_w8a8_workspace_size.argtypes = [u32] * 3 + [i32]
+        L.kaio_linear_w8a8_workspace_size.restype = ctypes.c_size_t
+        L.kaio_moe_w4a16.argtypes = [vp] * 4 + [u32] * 2 + [i32, ctypes.c_int, vp, ctypes.c_size_t, vp]
+        L.kaio_moe_w4a16.restype = ctypes.c_int
+        L.kaio_moe_w4a16_workspace_size.argtypes = [vp] + [u32] * 2
+        L.kaio_moe_w4a16_workspace_size.restype = ctypes.c_size_t
         L.kaio_rope_append.argtypes = [vp] * 7 + [u32, i32, vp, u32, u32, vp]
         L.kaio_rope_append.restype = ctypes.c_int
         L.kaio_paged_attention.argtypes = [vp] * 3 + [u32] * 3 + [ctypes.c_float, u32, u32, vp, ctypes.c_size_t, vp]
@@ -117,7 +138,9 @@ def _quick():
                 warnings.warn("_binding.so was built for another torch, calls go through ctypes: build again")
                 return _fast
             b.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                L.kaio_linear_w4a16, L.kaio_rope_append, L.kaio_paged_attention, L.kaio_paged_attention_workspace_size)])
+                L.kaio_linear_w4a16, L.kaio_rope_append, L.kaio_paged_attention, L.kaio_paged_attention_workspace_size,
+                L.kaio_quantize_rows, L.kaio_linear_w8a8, L.kaio_linear_w8a8_workspace_size, L.kaio_moe_w4a16,
+                L.kaio_moe_w4a16_workspace_size)])
             _fast = b
     return _fast
 
@@ -355,6 +378,189 @@ def kaio_linear_w4a16(x, w, s, bias=None, activation="none", residual=None, y=No
                                    None if bias is None else bias.data_ptr(),
                                    None if residual is None else residual.data_ptr(), y.data_ptr(),
                                    M, N, K, GROUP_SIZE, ACTIVATION_CODES[activation], _stream(dev, stream)))
+    return y
+
+
+def _like(t, name, dtypes, device, shape):
+    _tensor(t, name, dtypes, device, rank=len(shape), any_offset=True)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _scratch(need, workspace, device, stream):
+    """The workspace of a call that needs ``need`` bytes: the caller's, checked, or one of its own."""
+    import torch
+    if workspace is not None:
+        return _tensor(workspace, "workspace", (torch.uint8,), device, rank=1, any_offset=True)
+    return _allocate(device, stream, lambda: torch.empty((need,), dtype=torch.uint8, device=device)) if need else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kaio_quantize_rows(x, q=None, scale=None, stream=None):
+    """Rows rounded to 8 bits; returns (q int8[M, K], scale f32[M]).
+
+    x f16 or bf16 [M, K], K a multiple of 16: scale = max |row| / 127, q = round(127 x / max |row|), ties to even.  A row
+    with an infinity or a NaN has scale NaN and q 0.
+    """
+    fast = _fast or _quick()
+    if fast and stream is None:
+        r = fast.quantize_rows(x, q, scale)
+        if r is not None:
+            return r
+    import torch
+    _tensor(x, "x", (torch.float16, torch.bfloat16), any_offset=True)
+    dev = x.device
+    M, K = x.shape
+    if K % 16:
+        raise ValueError(f"K ({K}) must be a multiple of 16")
+    if q is None:
+        q = _allocate(dev, stream, lambda: torch.empty((M, K), dtype=torch.int8, device=dev))
+    if scale is None:
+        scale = _allocate(dev, stream, lambda: torch.empty((M,), dtype=torch.float32, device=dev))
+    _like(q, "q", (torch.int8,), dev, (M, K))
+    _like(scale, "scale", (torch.float32,), dev, (M,))
+    if max(M, K) >= 2 ** 32:
+        raise ValueError("dimension exceeds u32")
+    _check(lib().kaio_quantize_rows(2 if x.dtype == torch.float16 else 1, x.data_ptr(), q.data_ptr(), scale.data_ptr(), M, K,
+                                    _stream(dev, stream)))
+    return q, scale
+
+
+def kaio_linear_w8a8(x, w, w_scale, x_scale=None, bias=None, activation="none", residual=None, y=None, dtype=None,
+                     workspace=None, stream=None):
+    """y = act(x_scale * w_scale * (x . w^T) + bias) + residual, summed in integers, one rounding; returns y [M, N].
+
+    w int8 [N, K] with w_scale f32 [N], K a multiple of 16.  x int8 [M, K] with x_scale f32 [M], or f16 or bf16 [M, K]
+    without, then rounded here as by kaio_quantize_rows.  y, bias [N] and residual [M, N] are in x's dtype; for int8 x in
+    ``dtype``, else the dtype of y, residual or bias, the first that is given, else f16.  ``y`` may be ``residual`` itself
+    (updated in place).  ``workspace`` (uint8) is allocated here when it is needed and not given.
+    """
+    fast = _fast or _quick()
+    if fast and stream is None and dtype is None:
+        r = fast.linear8(x, w, w_scale, x_scale, bias, ACTIVATION_CODES.get(activation, -1), residual, y, workspace)
+        if r is not None:
+            return r
+    import torch
+    kinds = (torch.float16, torch.bfloat16)
+    _tensor(x, "x", (torch.int8,) if x_scale is not None else kinds, any_offset=True)
+    dev = x.device
+    M, K = x.shape
+    _tensor(w, "w", (torch.int8,), dev, any_offset=True)
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"K mismatch between inputs: x is [{M}, {K}], w is [{N}, {w.shape[1]}]")
+    if K % 16:
+        raise ValueError(f"K ({K}) must be a multiple of 16")
+    _like(w_scale, "w_scale", (torch.float32,), dev, (N,))
+    if x_scale is not None:
+        _like(x_scale, "x_scale", (torch.float32,), dev, (M,))
+        if dtype is None:
+            dtype = next((t.dtype for t in (y, residual, bias) if isinstance(t, torch.Tensor)), torch.float16)
+    elif dtype not in (None, x.dtype):
+        raise TypeError(f"dtype must be x's, {x.dtype}, got {dtype}")
+    else:
+        dtype = x.dtype
+    if dtype not in kinds:
+        raise TypeError(f"dtype must be one of {kinds}, got {dtype}")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}: one of {tuple(ACTIVATION_CODES)}")
+    if bias is not None:
+        _like(bias, "bias", (dtype,), dev, (N,))
+    if residual is not None:
+        _like(residual, "residual", (dtype,), dev, (M, N))
+    if y is None:
+        y = _allocate(dev, stream, lambda: torch.empty((M, N), dtype=dtype, device=dev))
+    _like(y, "y", (dtype,), dev, (M, N))
+    if max(M, N, K) >= 2 ** 32:
+        raise ValueError("dimension exceeds u32")
+    need = lib().kaio_linear_w8a8_workspace_size(M, N, K, int(x_scale is not None))
+    workspace = _scratch(need, workspace, dev, stream)
+    _check(lib().kaio_linear_w8a8(2 if dtype == torch.float16 else 1, x.data_ptr(), _ptr(x_scale), w.data_ptr(),
+                                  w_scale.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), M, N, K,
+                                  ACTIVATION_CODES[activation], _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                  _stream(dev, stream)))
+    return y
+
+
+class KaioExperts:
+    """The weights of a mixture-of-experts feed-forward (kaio_experts of include/kaio.h).
+
+    router          f16 [experts, hidden]
+    w_gate, w_up    packed INT4 as int32/uint32 [experts, hidden/8, inner]; s_gate, s_up f16 [experts, hidden/128, inner]
+    w_down          packed INT4 as int32/uint32 [experts, inner/8, hidden]; s_down f16 [experts, inner/128, hidden]
+
+    Holds the tensors; made once and kept while they live, as only their addresses and shapes are taken here.
+    """
+
+    def __init__(self, router, w_gate, s_gate, w_up, s_up, w_down, s_down):
+        import torch
+        f16, u32 = (torch.float16,), _u32_dtypes()
+        _tensor(router, "router", f16, any_offset=True)
+        dev = router.device
+        experts, hidden = router.shape
+        _tensor(w_gate, "w_gate", u32, dev, rank=3, any_offset=True)
+        inner = w_gate.shape[2]
+        if hidden % GROUP_SIZE or inner % GROUP_SIZE or not (experts and hidden and inner):
+            raise ValueError(f"hidden ({hidden}) and inner ({inner}) must be positive multiples of group_size "
+                             f"({GROUP_SIZE}), and there must be experts")
+        if max(experts, hidden, inner) >= 2 ** 31:
+            raise ValueError("dimension exceeds i32")
+        for t, name, k, n in ((w_gate, "gate", hidden, inner), (w_up, "up", hidden, inner), (w_down, "down", inner, hidden)):
+            _like(t, "w_" + name, u32, dev, (experts, k // 8, n))
+        for t, name, k, n in ((s_gate, "gate", hidden, inner), (s_up, "up", hidden, inner), (s_down, "down", inner, hidden)):
+            _like(t, "s_" + name, f16, dev, (experts, k // GROUP_SIZE, n))
+        self.router, self.w_gate, self.s_gate, self.w_up, self.s_up, self.w_down, self.s_down = \
+            router, w_gate, s_gate, w_up, s_up, w_down, s_down
+        self.device, self.experts, self.hidden, self.inner = dev, experts, hidden, inner
+        self._c = _Experts(*[t.data_ptr() for t in (router, w_gate, s_gate, w_up, s_up, w_down, s_down)],
+                           experts, hidden, inner, GROUP_SIZE)
+        self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
+        self._index = dev.index
+
+
+def kaio_moe_w4a16(x, experts, top_k, normalize=True, activation="silu", residual=None, y=None, workspace=None, stream=None):
+    """A mixture-of-experts feed-forward for a few tokens; returns y f16 [T, hidden].
+
+    x f16 [T, hidden]; each token goes to the ``top_k`` experts of largest <x, router row> (ties: the lowest index), with
+    their softmax over all experts as weights, or over the chosen ones with ``normalize``:
+    y = sum of weight * (act(x . gate) * (x . up)) . down, + residual.  ``y`` may be ``residual`` itself.  ``workspace``
+    (uint8) is allocated here when not given.
+    """
+    if not isinstance(experts, KaioExperts):
+        raise TypeError("experts must be a KaioExperts")
+    fast = _fast or _quick()
+    if fast and stream is None:
+        r = fast.moe(x, experts._addr, experts._index, top_k, bool(normalize), ACTIVATION_CODES.get(activation, -1), residual,
+                     y, workspace)
+        if r is not None:
+            return r
+    import torch
+    f16 = (torch.float16,)
+    dev = experts.device
+    _tensor(x, "x", f16, dev, any_offset=True)
+    T = x.shape[0]
+    _like(x, "x", f16, dev, (T, experts.hidden))
+    if not 1 <= top_k <= experts.experts:
+        raise ValueError(f"top_k ({top_k}) must be 1 to experts ({experts.experts})")
+    if activation not in ACTIVATION_CODES:
+        raise ValueError(f"unknown activation {activation!r}: one of {tuple(ACTIVATION_CODES)}")
+    if residual is not None:
+        _like(residual, "residual", f16, dev, x.shape)
+    if y is None:
+        y = _allocate(dev, stream, lambda: torch.empty_like(x))
+    _like(y, "y", f16, dev, x.shape)
+    if T >= 2 ** 32:
+        raise ValueError("dimension exceeds u32")
+    need = lib().kaio_moe_w4a16_workspace_size(experts._ref, T, top_k)
+    workspace = _scratch(need, workspace, dev, stream)
+    _check(lib().kaio_moe_w4a16(experts._ref, x.data_ptr(), _ptr(residual), y.data_ptr(), T, top_k, int(bool(normalize)),
+                                ACTIVATION_CODES[activation], _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                _stream(dev, stream)))
     return y
 
 

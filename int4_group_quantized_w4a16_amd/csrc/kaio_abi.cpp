@@ -256,6 +256,18 @@ int code_of(const E& e) {
   return code;
 }
 
+// Whether sizes that the operation defines and offers fit its launches.
+bool moe_fits(const kaio_experts* e, uint32_t tokens, uint32_t top_k) {
+  if (tokens == 0 || tokens > kaio::kMoeMaxTokens || top_k == 0 || top_k > e->experts || top_k > kaio::kMoeMaxTop ||
+      e->experts > kaio::kMoeMaxExperts || e->hidden == 0 || e->inner == 0 || e->hidden % 128 != 0 || e->inner % 128 != 0 ||
+      e->hidden >= kaio::kMaxK || e->inner >= kaio::kMaxK)
+    return false;
+  uint64_t bytes = 0;
+  const kaio::MoePlan plan = kaio::moe_plan(tokens, e->experts, e->hidden, e->inner, top_k);
+  return bytes_of((uint64_t)e->experts * e->hidden, e->inner, 1, &bytes) && plan.bytes < (1ull << 62) &&
+         plan.slots * (e->inner / 64) <= kaio::kMaxWorkgroups && plan.splits * (e->hidden / 64) <= kaio::kMaxWorkgroups;
+}
+
 // The checks of a paged cache that need no pointers: dtype and sizes.
 kaio_status check_paged_sizes(const char* op, const kaio_paged_kv* kv) {
   if (!kv) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "kv is null");
@@ -626,6 +638,177 @@ kaio_status kaio_paged_attention(const kaio_paged_kv* kv, const void* q, void* o
   const hipError_t e = plan.stream ? kaio::launch_attention_stream(p, plan, st) : kaio::launch_attention_tile(p, plan, st);
   if (e != hipSuccess || !plan.split) return launched(op, e);
   return launched(op, kaio::launch_attention_join(p, plan, st));
+}
+
+kaio_status kaio_quantize_rows(kaio_dtype dtype, const void* x, int8_t* q, float* scale, uint32_t m, uint32_t k,
+                               void* stream) {
+  static const char* op = "quantize_rows";
+  const int type = code_of(dtype);
+  if (type != KAIO_DTYPE_F16 && type != KAIO_DTYPE_BF16)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "unsupported dtype %d (f16, bf16)", type);
+  if (k % 16 != 0) return fail(KAIO_ERR_INVALID_PROBLEM, op, "K (%u) must be a multiple of 16", k);
+  if (m == 0) return ok();
+  uint64_t x_bytes = 0;
+  if (!bytes_of(m, k, 2, &x_bytes) || m > kaio::kMaxWorkgroups || k >= kaio::kMaxK)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (m=%u, k=%u)", m, k);
+  const struct { const void* p; const char* name; bool used; } all[3] = {
+      {x, "input x", k > 0}, {q, "output q", k > 0}, {scale, "output scale", true}};
+  for (const auto& a : all)
+    if (a.used && !a.p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is null", a.name);
+  for (const auto& a : all)
+    if (a.used && !aligned16(a.p)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is not 16-byte aligned", a.name);
+  const Range ro[2] = {range(q, x_bytes / 2, "q"), range(scale, (uint64_t)m * 4, "scale")};
+  const Range ri[1] = {range(x, x_bytes, "x")};
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 2, ri, 1, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output %s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  return launched(op, kaio::launch_quantize_rows(static_cast<const uint16_t*>(x), type == KAIO_DTYPE_BF16,
+                                                 reinterpret_cast<uint8_t*>(q), scale, m, k, static_cast<hipStream_t>(stream)));
+}
+
+size_t kaio_linear_w8a8_workspace_size(uint32_t m, uint32_t n, uint32_t k, int32_t int8_x) {
+  if (k % 16 != 0 || k > kaio::kLinear8MaxK || m == 0 || n == 0 || int8_x) return 0;
+  return kaio::linear8_workspace(m, k);
+}
+
+kaio_status kaio_linear_w8a8(kaio_dtype dtype, const void* x, const float* x_scale, const int8_t* w, const float* w_scale,
+                             const void* bias, const void* residual, void* y, uint32_t m, uint32_t n, uint32_t k,
+                             kaio_activation activation, void* workspace, size_t workspace_bytes, void* stream) {
+  static const char* op = "linear_w8a8";
+  const int type = code_of(dtype), act = code_of(activation);
+  if (type != KAIO_DTYPE_F16 && type != KAIO_DTYPE_BF16)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "unsupported dtype %d (f16, bf16)", type);
+  if (act < KAIO_ACT_NONE || act > KAIO_ACT_SILU) return fail(KAIO_ERR_UNSUPPORTED, op, "unknown activation %d", act);
+  if (k % 16 != 0) return fail(KAIO_ERR_INVALID_PROBLEM, op, "K (%u) must be a multiple of 16", k);
+  if (k > kaio::kLinear8MaxK)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "K (%u) must be at most %u, which 32-bit sums hold", k, kaio::kLinear8MaxK);
+  if (m == 0 || n == 0) return ok();
+  const bool rounds = !x_scale;   // x is 16-bit and rounded here
+  uint64_t x_bytes = 0, w_bytes = 0, out_bytes = 0;
+  if (!bytes_of(m, k, rounds ? 2 : 1, &x_bytes) || !bytes_of(n, k, 1, &w_bytes) || !bytes_of(m, n, 2, &out_bytes) ||
+      kaio::linear8_wgs(m, n) > kaio::kMaxWorkgroups || m > kaio::kMaxWorkgroups || n >= kaio::kMaxN)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (m=%u, n=%u, k=%u)", m, n, k);
+  const uint64_t need = kaio_linear_w8a8_workspace_size(m, n, k, !rounds);
+  const struct { const void* p; const char* name; bool needed, used; } all[8] = {
+      {y, "output y", true, true}, {x, "input x", k > 0, k > 0}, {w, "input w", k > 0, k > 0},
+      {w_scale, "input w_scale", true, true}, {x_scale, "input x_scale", false, !rounds}, {bias, "input bias", false, bias != nullptr},
+      {residual, "input residual", false, residual != nullptr}, {workspace, "workspace", need > 0, need > 0}};
+  for (const auto& a : all)
+    if (a.needed && !a.p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is null", a.name);
+  if (workspace_bytes < need)
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace_bytes (%zu) < %llu needed", workspace_bytes,
+                (unsigned long long)need);
+  for (const auto& a : all)
+    if (a.used && !aligned16(a.p)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s is not 16-byte aligned", a.name);
+  const Range ro[2] = {range(y, out_bytes, "y"), range(workspace, need, "workspace")};
+  const Range ri[6] = {range(x, x_bytes, "x"), range(w, w_bytes, "w"), range(w_scale, (uint64_t)n * 4, "w_scale"),
+                       range(x_scale, rounds ? 0 : (uint64_t)m * 4, "x_scale"), range(bias, bias ? (uint64_t)n * 2 : 0, "bias"),
+                       range(residual, residual && residual != y ? out_bytes : 0, "residual")};
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 2, ri, 6, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  kaio::Linear8 p;
+  p.x = static_cast<const int8_t*>(x);
+  p.xs = x_scale;
+  p.w = w;
+  p.ws = w_scale;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.y = static_cast<uint16_t*>(y);
+  p.m = m; p.n = n; p.k = k;
+  p.act = act;
+  p.bf16 = type == KAIO_DTYPE_BF16;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (rounds) {
+    uint8_t* const q = static_cast<uint8_t*>(workspace);
+    float* const scale = reinterpret_cast<float*>(q + kaio::linear8_rows_bytes(m, k));
+    if (hipError_t e = kaio::launch_quantize_rows(static_cast<const uint16_t*>(x), p.bf16, q, scale, m, k, st))
+      return launched(op, e);
+    p.x = reinterpret_cast<const int8_t*>(q);
+    p.xs = scale;
+  }
+  return launched(op, kaio::launch_linear_w8a8(p, st));
+}
+
+size_t kaio_moe_w4a16_workspace_size(const kaio_experts* e, uint32_t tokens, uint32_t top_k) {
+  if (!e || !moe_fits(e, tokens, top_k)) return 0;
+  return kaio::moe_plan(tokens, e->experts, e->hidden, e->inner, top_k).bytes;
+}
+
+kaio_status kaio_moe_w4a16(const kaio_experts* e, const void* x, const void* residual, void* y, uint32_t tokens,
+                           uint32_t top_k, int32_t normalize, kaio_activation activation, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  static const char* op = "moe_w4a16";
+  if (!e) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "experts is null");
+  const int act = code_of(activation);
+  if (e->group_size != 128)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "group_size (%u) must be 128 (locked by the kernel contract)", e->group_size);
+  if (act < KAIO_ACT_NONE || act > KAIO_ACT_SILU) return fail(KAIO_ERR_UNSUPPORTED, op, "unknown activation %d", act);
+  if (e->experts > kaio::kMoeMaxExperts || top_k > kaio::kMoeMaxTop)
+    return fail(KAIO_ERR_UNSUPPORTED, op, "experts (%u) and top_k (%u) must be at most %u and %u", e->experts, top_k,
+                kaio::kMoeMaxExperts, kaio::kMoeMaxTop);
+  if (e->hidden % 128 != 0 || e->inner % 128 != 0 || e->hidden == 0 || e->inner == 0)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "hidden (%u) and inner (%u) must be positive multiples of group_size (128)",
+                e->hidden, e->inner);
+  if (top_k == 0 || top_k > e->experts)
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "top_k (%u) must be 1 to experts (%u)", top_k, e->experts);
+  if (tokens == 0) return ok();
+  if (!moe_fits(e, tokens, top_k))
+    return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (tokens=%u, experts=%u, hidden=%u, inner=%u)",
+                tokens, e->experts, e->hidden, e->inner);
+  const kaio::MoePlan plan = kaio::moe_plan(tokens, e->experts, e->hidden, e->inner, top_k);
+  const uint64_t rows = (uint64_t)tokens * e->hidden * 2, all_w = (uint64_t)e->experts * e->hidden * e->inner;
+  const struct { const void* p; const char* name; uint64_t bytes; } ins[9] = {
+      {x, "x", rows}, {e->router, "router", (uint64_t)e->experts * e->hidden * 2},
+      {e->w_gate, "w_gate", all_w / 2}, {e->w_up, "w_up", all_w / 2}, {e->w_down, "w_down", all_w / 2},
+      {e->s_gate, "s_gate", all_w / 64}, {e->s_up, "s_up", all_w / 64}, {e->s_down, "s_down", all_w / 64},
+      {residual, "residual", residual && residual != y ? rows : 0}};
+  for (int i = 0; i < 8; ++i)
+    if (!ins[i].p) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input %s is null", ins[i].name);
+  if (!y) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output y is null");
+  if (!workspace) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace is null");
+  if (workspace_bytes < plan.bytes)
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace_bytes (%zu) < %llu needed", workspace_bytes,
+                (unsigned long long)plan.bytes);
+  for (const auto& i : ins)
+    if (!aligned16(i.p)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "input %s is not 16-byte aligned", i.name);
+  if (!aligned16(y)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "output y is not 16-byte aligned");
+  if (!aligned16(workspace)) return fail(KAIO_ERR_INVALID_ARGUMENT, op, "workspace is not 16-byte aligned");
+  const Range ro[2] = {range(y, rows, "y"), range(workspace, plan.bytes, "workspace")};
+  Range ri[9];
+  for (int i = 0; i < 9; ++i) ri[i] = range(ins[i].p, ins[i].bytes, ins[i].name);
+  const Range* other = nullptr;
+  if (const Range* o = overlap(ro, 2, ri, 9, &other))
+    return fail(KAIO_ERR_INVALID_ARGUMENT, op, "%s overlaps %s", o->name, other->name);
+  if (kaio_status st = check_device(op)) return st;
+  (void)hipGetLastError();
+  kaio::Moe p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.router = static_cast<const uint16_t*>(e->router);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.w_gate = e->w_gate; p.w_up = e->w_up; p.w_down = e->w_down;
+  p.s_gate = static_cast<const uint16_t*>(e->s_gate);
+  p.s_up = static_cast<const uint16_t*>(e->s_up);
+  p.s_down = static_cast<const uint16_t*>(e->s_down);
+  p.y = static_cast<uint16_t*>(y);
+  p.tokens = tokens; p.experts = e->experts; p.hidden = e->hidden; p.inner = e->inner; p.top_k = top_k;
+  p.act = act;
+  p.normalize = normalize != 0;
+  p.slots = (uint32_t)plan.slots;
+  p.splits = (uint32_t)plan.splits;
+  char* const at = static_cast<char*>(workspace);
+  p.scores = reinterpret_cast<double*>(at);
+  p.route = reinterpret_cast<kaio::MoeRoute*>(at + plan.route);
+  p.share = reinterpret_cast<float*>(at + plan.share);
+  p.active = reinterpret_cast<uint32_t*>(at + plan.active);
+  p.arrived = reinterpret_cast<uint32_t*>(at + plan.arrived);
+  p.h = reinterpret_cast<uint16_t*>(at + plan.h);
+  p.partial = reinterpret_cast<float*>(at + plan.partial);
+  return launched(op, kaio::launch_moe_w4a16(p, static_cast<hipStream_t>(stream)));
 }
 
 const char* kaio_last_error(void) { return g_last_error.c_str(); }

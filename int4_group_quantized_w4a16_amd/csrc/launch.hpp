@@ -209,6 +209,85 @@ constexpr LinearForm linear_form(uint32_t m, uint32_t n, uint32_t k) {
 constexpr uint64_t linear_wgs(uint64_t m, uint64_t n) { return (m + 63) / 64 * ((n + 15) / 16); }
 hipError_t launch_linear_w4a16(const LinearProblem& p, hipStream_t stream);
 
+// Rows of 16-bit numbers rounded to int8, each with its scale.
+hipError_t launch_quantize_rows(const uint16_t* x, bool bf16, uint8_t* q, float* scale, uint32_t m, uint32_t k,
+                                hipStream_t stream);
+
+// y = act(xs ws (x . w^T) + bias) + residual in 8-bit integers; bias and residual may be null.
+struct Linear8 {
+  const int8_t* x;            // [m, k]
+  const float* xs;            // [m]
+  const int8_t* w;            // [n, k]
+  const float* ws;            // [n]
+  const uint16_t* bias;       // [n], 16-bit as y
+  const uint16_t* residual;   // [m, n]
+  uint16_t* y;                // [m, n]
+  uint32_t m, n, k;
+  int act;                    // kaio_activation
+  bool bf16;
+};
+constexpr uint32_t kLinear8MaxK = (1u << 17) - 16;   // |sum| <= 2^14 k stays below 2^31
+// bytes of m rounded rows of k, then of their scales
+constexpr uint64_t linear8_rows_bytes(uint64_t m, uint64_t k) { return m * k; }
+constexpr uint64_t linear8_workspace(uint64_t m, uint64_t k) { return linear8_rows_bytes(m, k) + (4 * m + 15) / 16 * 16; }
+// a bound on the workgroups of a call in any form
+constexpr uint64_t linear8_wgs(uint64_t m, uint64_t n) { return (m + 63) / 64 * ((n + 63) / 64); }
+hipError_t launch_linear_w8a8(const Linear8& p, hipStream_t stream);
+
+// Mixture of experts.  Tokens are taken in blocks of kMoeBlock, each of which has its own active experts.
+constexpr uint32_t kMoeBlock = 64, kMoeMaxExperts = 512, kMoeMaxTop = 16, kMoeMaxTokens = 1u << 17;
+struct MoeRoute {             // an active expert: its tokens (bits of the block), and its first row of h in the block
+  uint64_t mask;
+  uint32_t expert, first;
+};
+struct Moe {
+  const uint16_t *x, *router, *residual;        // [tokens, hidden], [experts, hidden], [tokens, hidden] or null
+  const uint32_t *w_gate, *w_up, *w_down;       // [experts, hidden / 8, inner] (2), [experts, inner / 8, hidden]
+  const uint16_t *s_gate, *s_up, *s_down;       // scales, a row per 128 of k
+  uint16_t* y;
+  uint32_t tokens, experts, hidden, inner, top_k;
+  int act;
+  bool normalize;
+  uint32_t slots, splits;     // most active experts of a block; parts of the down product
+  // workspace
+  double* scores;             // [tokens, experts]
+  MoeRoute* route;            // [blocks, slots]
+  float* share;               // [blocks, slots, kMoeBlock]
+  uint32_t *active, *arrived; // [blocks], [blocks, hidden / 64]
+  uint16_t* h;                // [tokens * top_k, inner]
+  float* partial;             // [splits, tokens, hidden] where splits > 1
+};
+struct MoePlan {
+  uint64_t blocks, slots, splits;
+  uint64_t route, share, active, arrived, h, partial, bytes;   // offsets in the workspace (scores come first)
+};
+constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, uint64_t inner, uint64_t top_k) {
+  MoePlan a{};
+  a.blocks = (tokens + kMoeBlock - 1) / kMoeBlock;
+  const uint64_t pairs = (tokens < kMoeBlock ? tokens : kMoeBlock) * top_k;
+  a.slots = pairs < experts ? pairs : experts;
+  // two workgroups of the down product per compute unit, of two units for each wave at least
+  const uint64_t strips = hidden / 64 * a.blocks, units = a.slots * (inner / 128);
+  const uint64_t fill = (2 * kComputeUnits + strips - 1) / strips, most = units / 16 ? units / 16 : 1;
+  a.splits = fill < most ? fill : most;
+  uint64_t at = 0;
+  const auto take = [&at](uint64_t bytes) {
+    const uint64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  take(tokens * experts * 8);
+  a.route = take(a.blocks * a.slots * sizeof(MoeRoute));
+  a.share = take(a.blocks * a.slots * kMoeBlock * 4);
+  a.active = take(a.blocks * 4);
+  a.arrived = take(a.blocks * (hidden / 64) * 4);
+  a.h = take(tokens * top_k * inner * 2);
+  a.partial = take(a.splits > 1 ? a.splits * tokens * hidden * 4 : 0);
+  a.bytes = at;
+  return a;
+}
+hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream);
+
 constexpr uint32_t kMaxAxes = 8;
 struct RopeAppend {
   PagedKV kv;

@@ -28,6 +28,11 @@ decltype(&kaio_linear_w4a16) g_linear;
 decltype(&kaio_rope_append) g_rope;
 decltype(&kaio_paged_attention) g_attention;
 decltype(&kaio_paged_attention_workspace_size) g_workspace;
+decltype(&kaio_quantize_rows) g_quantize;
+decltype(&kaio_linear_w8a8) g_linear8;
+decltype(&kaio_linear_w8a8_workspace_size) g_linear8_workspace;
+decltype(&kaio_moe_w4a16) g_moe;
+decltype(&kaio_moe_w4a16_workspace_size) g_moe_workspace;
 
 // the tensor behind obj, or null if it is not one that the fast path takes
 const at::Tensor* tensor(PyObject* obj, at::ScalarType type, int64_t rank, int device) {
@@ -200,14 +205,147 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(linear, rope_append, paged_attention, workspace_size): addresses of the C entry points
+// the tensor behind obj, of the given shape; absent: obj is None
+const at::Tensor* shaped(PyObject* obj, at::ScalarType type, at::IntArrayRef shape, int device) {
+  const at::Tensor* t = tensor(obj, type, (int64_t)shape.size(), device);
+  return t && t->sizes() == shape ? t : nullptr;
+}
+bool optional(PyObject* obj, at::ScalarType type, at::IntArrayRef shape, int device, const at::Tensor** out) {
+  *out = nullptr;
+  return obj == Py_None || (*out = shaped(obj, type, shape, device));
+}
+// the caller's tensor, or one made here
+bool output(PyObject* obj, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& like, at::Tensor* made,
+            const at::Tensor** out) {
+  if (obj != Py_None) return (*out = shaped(obj, type, shape, like.get_device())) != nullptr;
+  *made = at::empty(shape, like.options().dtype(type));
+  *out = made;
+  return true;
+}
+bool scratch_of(PyObject* obj, size_t need, const at::Tensor& like, at::Tensor* made, const at::Tensor** out) {
+  *out = nullptr;
+  if (obj != Py_None) return (*out = tensor(obj, at::kByte, 1, like.get_device())) != nullptr;
+  if (need) {
+    *made = at::empty({(int64_t)need}, like.options().dtype(at::kByte));
+    *out = made;
+  }
+  return true;
+}
+PyObject* result(PyObject* given, at::Tensor&& made) {
+  if (given == Py_None) return THPVariable_Wrap(std::move(made));
+  Py_INCREF(given);
+  return given;
+}
+void* data(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
+bool half_type(const at::Tensor& t) { return t.scalar_type() == at::kHalf || t.scalar_type() == at::kBFloat16; }
+kaio_dtype dtype_of(at::ScalarType t) { return t == at::kHalf ? KAIO_DTYPE_F16 : KAIO_DTYPE_BF16; }
+
+// quantize_rows(x, q | None, scale | None)
+PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 3 || !g_quantize || !THPVariable_Check(a[0])) return none();
+    const at::Tensor& x = THPVariable_Unpack(a[0]);
+    if (!x.defined() || !x.is_cuda() || !half_type(x) || x.dim() != 2 || !x.is_contiguous()) return none();
+    const int64_t M = x.size(0), K = x.size(1);
+    if (!fits(M) || !fits(K)) return none();
+    void* stream;
+    if (!stream_of(x.get_device(), &stream)) return none();
+    at::Tensor made_q, made_s;
+    const at::Tensor *q, *s;
+    if (!output(a[1], at::kChar, {M, K}, x, &made_q, &q) || !output(a[2], at::kFloat, {M}, x, &made_s, &s)) return none();
+    if (g_quantize(dtype_of(x.scalar_type()), x.data_ptr(), static_cast<int8_t*>(q->data_ptr()),
+                   static_cast<float*>(s->data_ptr()), (uint32_t)M, (uint32_t)K, stream) != KAIO_OK)
+      return none();
+    PyObject *pq = result(a[1], std::move(made_q)), *ps = result(a[2], std::move(made_s));
+    PyObject* both = PyTuple_Pack(2, pq, ps);
+    Py_XDECREF(pq);
+    Py_XDECREF(ps);
+    return both;
+  });
+}
+
+// linear8(x, w, w_scale, x_scale | None, bias | None, activation code, residual | None, y | None, workspace | None);
+PyObject* linear8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 9 || !g_linear8 || !THPVariable_Check(a[0])) return none();
+    const at::Tensor& x = THPVariable_Unpack(a[0]);
+    if (!x.defined() || !x.is_cuda() || x.dim() != 2 || !x.is_contiguous()) return none();
+    const int dev = x.get_device();
+    const bool rounded = a[3] != Py_None;
+    at::ScalarType type = x.scalar_type();
+    if (rounded) {   // the type of y, residual or bias, the first that is there
+      if (type != at::kChar) return none();
+      PyObject* const of = a[7] != Py_None ? a[7] : a[6] != Py_None ? a[6] : a[4];
+      if (of != Py_None && !THPVariable_Check(of)) return none();
+      type = of == Py_None ? at::kHalf : THPVariable_Unpack(of).scalar_type();
+    }
+    if (type != at::kHalf && type != at::kBFloat16) return none();
+    const at::Tensor* w = tensor(a[1], at::kChar, 2, dev);
+    if (!w) return none();
+    const int64_t M = x.size(0), K = x.size(1), N = w->size(0);
+    if (w->size(1) != K || !fits(M) || !fits(N) || !fits(K)) return none();
+    const at::Tensor *ws = shaped(a[2], at::kFloat, {N}, dev), *xs, *b, *r, *y, *scratch;
+    if (!ws || !optional(a[3], at::kFloat, {M}, dev, &xs) || !optional(a[4], type, {N}, dev, &b) ||
+        !optional(a[6], type, {M, N}, dev, &r))
+      return none();
+    const long act = PyLong_AsLong(a[5]);
+    if (act < 0) {
+      PyErr_Clear();
+      return none();
+    }
+    void* stream;
+    if (!stream_of(dev, &stream)) return none();
+    at::Tensor made, made_scratch;
+    const size_t need = g_linear8_workspace((uint32_t)M, (uint32_t)N, (uint32_t)K, rounded);
+    if (!output(a[7], type, {M, N}, x, &made, &y) || !scratch_of(a[8], need, x, &made_scratch, &scratch)) return none();
+    if (g_linear8(dtype_of(type), x.data_ptr(), static_cast<const float*>(data(xs)), static_cast<const int8_t*>(w->data_ptr()),
+                  static_cast<const float*>(ws->data_ptr()), data(b), data(r), y->data_ptr(), (uint32_t)M, (uint32_t)N,
+                  (uint32_t)K, static_cast<kaio_activation>(act), data(scratch), scratch ? (size_t)scratch->numel() : 0,
+                  stream) != KAIO_OK)
+      return none();
+    return result(a[7], std::move(made));
+  });
+}
+
+// moe(x, experts address, device, top_k, normalize, activation code, residual | None, y | None, workspace | None)
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 9 || !g_moe) return none();
+    const auto* e = static_cast<const kaio_experts*>(PyLong_AsVoidPtr(a[1]));
+    const int dev = (int)PyLong_AsLong(a[2]);
+    const long top = PyLong_AsLong(a[3]), act = PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      return none();
+    }
+    if (!e || top < 1 || !fits(top) || act < 0) return none();
+    const at::Tensor* x = tensor(a[0], at::kHalf, 2, dev);
+    if (!x || x->size(1) != e->hidden || !fits(x->size(0))) return none();
+    const uint32_t T = (uint32_t)x->size(0);
+    const at::Tensor *r, *y, *scratch;
+    if (!optional(a[6], at::kHalf, x->sizes(), dev, &r)) return none();
+    void* stream;
+    if (!stream_of(dev, &stream)) return none();
+    at::Tensor made, made_scratch;
+    const size_t need = g_moe_workspace(e, T, (uint32_t)top);
+    if (!output(a[7], at::kHalf, x->sizes(), *x, &made, &y) || !scratch_of(a[8], need, *x, &made_scratch, &scratch)) return none();
+    if (g_moe(e, x->data_ptr(), data(r), y->data_ptr(), T, (uint32_t)top, a[4] == Py_True, static_cast<kaio_activation>(act),
+              data(scratch), scratch ? (size_t)scratch->numel() : 0, stream) != KAIO_OK)
+      return none();
+    return result(a[7], std::move(made));
+  });
+}
+
+// bind(linear, rope_append, paged_attention, its workspace size, quantize_rows, linear_w8a8, its workspace size,
+// moe_w4a16, its workspace size): addresses of the C entry points
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  constexpr Py_ssize_t kEntries = 9;
+  if (n != kEntries) {
+    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -215,11 +353,17 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_rope = reinterpret_cast<decltype(g_rope)>(p[1]);
   g_attention = reinterpret_cast<decltype(g_attention)>(p[2]);
   g_workspace = reinterpret_cast<decltype(g_workspace)>(p[3]);
+  g_quantize = reinterpret_cast<decltype(g_quantize)>(p[4]);
+  g_linear8 = reinterpret_cast<decltype(g_linear8)>(p[5]);
+  g_linear8_workspace = reinterpret_cast<decltype(g_linear8_workspace)>(p[6]);
+  g_moe = reinterpret_cast<decltype(g_moe)>(p[7]);
+  g_moe_workspace = reinterpret_cast<decltype(g_moe_workspace)>(p[8]);
   return none();
 }
 
 #define KAIO_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {KAIO_METHOD(linear), KAIO_METHOD(rope_append), KAIO_METHOD(attention), KAIO_METHOD(bind),
+PyMethodDef methods[] = {KAIO_METHOD(linear), KAIO_METHOD(rope_append), KAIO_METHOD(attention),
+                         KAIO_METHOD(quantize_rows), KAIO_METHOD(linear8), KAIO_METHOD(moe), KAIO_METHOD(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,190 @@
+"""The 8-bit product with its epilogue on the GPU against the oracle (tolerance: oracle.linear8.tolerance)."""
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_w4a16_amd as kaio
+from oracle import linear8 as ol
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float16, torch.bfloat16]
+STEP = {torch.float16: (2.0 ** -11, 2.0 ** -25), torch.bfloat16: (2.0 ** -8, 2.0 ** -120)}   # half a step; below that, absolute
+
+
+def inputs(m, n, k, seed, dtype, bias=True, residual=True, rounded=True):
+    r = np.random.default_rng(seed)
+    w = torch.from_numpy(r.integers(-128, 128, (n, k)).astype(np.int8))
+    ws = torch.from_numpy(r.uniform(1e-4, 5e-4, n).astype(np.float32))
+    if rounded:
+        x, xs = torch.from_numpy(r.integers(-128, 128, (m, k)).astype(np.int8)), torch.from_numpy(r.uniform(0.01, 0.05, m).astype(np.float32))
+    else:
+        x, xs = torch.from_numpy(r.standard_normal((m, k)) * r.uniform(0.2, 4, (m, 1))).to(dtype), None
+    b = torch.from_numpy(r.standard_normal(n)).to(dtype) if bias else None
+    res = torch.from_numpy(r.standard_normal((m, n))).to(dtype) if residual else None
+    return x, w, ws, xs, b, res
+
+
+def expected(x, w, ws, xs, b, res, act, dtype):
+    f64 = lambda t: None if t is None else t.double().numpy()
+    if xs is None:
+        xq, s = ol.quantize(f64(x))
+    else:
+        xq, s = x.numpy(), xs.numpy()
+    y, z, p = ol.linear(xq, s, w.numpy(), ws.numpy(), f64(b), act, f64(res))
+    return y, ol.tolerance(y, z, p, act, *STEP[dtype], f64(b), f64(res))
+
+
+def run_case(m, n, k, act="none", dtype=torch.float16, bias=True, residual=True, rounded=True, seed=0, in_place=False):
+    args = inputs(m, n, k, seed + m + n, dtype, bias, residual, rounded)
+    x, w, ws, xs, b, res = [None if t is None else t.to(DEV) for t in args]
+    y = res if in_place else torch.full((m, n), float("nan"), dtype=dtype, device=DEV)
+    got = kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, bias=b, activation=act, residual=res, y=y)
+    torch.cuda.synchronize()
+    assert got is y
+    want, tol = expected(*args, act, dtype)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"{(~(err <= tol)).sum()} of {err.size} outside tolerance, max ratio {np.nanmax(err / tol):.3f}"
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("m", [1, 20, 70, 300])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_activations(act, m, dtype):
+    run_case(m, 264, 512, act, dtype)
+    run_case(m, 133, 208, act, dtype, bias=False, rounded=False)
+
+
+@pytest.mark.parametrize("m", [1, 2, 8, 9, 16, 17, 31, 32, 33, 48, 61, 64, 65, 96, 97, 127, 128, 129, 193, 300])
+@pytest.mark.parametrize("n,k", [(64, 512), (100, 384), (77, 640), (260, 1040), (513, 16), (33, 4112)])
+def test_sizes(m, n, k):
+    run_case(m, n, k, "silu", bias=m % 2 == 0, residual=n % 2 == 0, dtype=TYPES[m % 2], rounded=(m + n) % 3 != 0)
+
+
+@pytest.mark.parametrize("k", [16, 32, 48, 64, 80, 112, 128, 144, 192, 240, 256, 272, 496, 528, 1008, 2064])
+@pytest.mark.parametrize("m,n", [(5, 72), (40, 130), (140, 260)])
+def test_every_end_of_the_sum(k, m, n):
+    run_case(m, n, k, bias=False, residual=False)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (5, 3, 256), (130, 7, 128), (8, 4096, 4096), (61, 1004, 4096), (260, 1000, 2688),
+                                   (1030, 520, 256), (700, 1300, 1024), (2049, 300, 128), (3, 9000, 256), (1024, 1024, 512)])
+@pytest.mark.parametrize("rounded", [True, False])
+def test_edges(m, n, k, rounded):
+    run_case(m, n, k, "gelu_tanh", rounded=rounded)
+    run_case(m, n, k, "none", TYPES[1], bias=False, residual=False, rounded=rounded)
+
+
+@pytest.mark.parametrize("m", [1, 4, 50, 100, 300])
+def test_in_place_residual_and_empty_sum(m):
+    run_case(m, 136, 256, "gelu", in_place=True)
+    run_case(m, 133, 256, "relu", TYPES[1], in_place=True, rounded=False)
+    for rounded in (True, False):
+        run_case(m, 72, 0, "relu", rounded=rounded)
+
+
+@pytest.mark.parametrize("m", [1, 20, 100, 260])
+def test_rounding_inside_is_the_two_calls(m):
+    for n, k, dtype in ((200, 512, TYPES[0]), (77, 4112, TYPES[1])):
+        x, w, ws, _, b, res = [None if t is None else t.to(DEV) for t in inputs(m, n, k, m, dtype, rounded=False)]
+        x[0] = 0
+        x[m // 2, 3] = float("nan")
+        q, s = kaio.kaio_quantize_rows(x)
+        one = kaio.kaio_linear_w8a8(x, w, ws, bias=b, activation="silu", residual=res)
+        two = kaio.kaio_linear_w8a8(q, w, ws, x_scale=s, bias=b, activation="silu", residual=res)
+        torch.cuda.synchronize()
+        assert one.dtype == dtype and torch.equal(one.view(torch.int16), two.view(torch.int16))
+        assert one[m // 2].isnan().all() and (m == 1 or not one[m - 1 if m // 2 != m - 1 else 0].isnan().any())
+
+
+@pytest.mark.parametrize("m", [1, 17, 70, 200])
+def test_largest_sums(m):
+    # every product 2^14: the sum is the largest that the length allows, and no 32-bit integer is left behind
+    k = 131056
+    x, w = torch.full((m, k), -128, dtype=torch.int8, device=DEV), torch.full((40, k), -128, dtype=torch.int8, device=DEV)
+    w[1] = 127
+    w[2, ::2] = 0
+    y = kaio.kaio_linear_w8a8(x, w, torch.full((40,), 2.0 ** -15, device=DEV), x_scale=torch.full((m,), 0.5, device=DEV))
+    torch.cuda.synchronize()
+    for col, total in ((0, 16384 * k), (1, -128 * 127 * k), (2, 16384 * k // 2)):
+        want = total * 2.0 ** -16
+        assert (y[:, col].double() - want).abs().max() <= 2.0 ** -11 * abs(want) + 2.0 ** -23 * abs(want)
+
+
+@pytest.mark.parametrize("m", [1, 20, 100, 300])
+def test_special_values(m):
+    x, w, ws, xs, b, res = inputs(m, 72, 256, 3, torch.float16)
+    x[:], res[:] = 0, 0
+    xs[0] = float("nan")
+    b[:8] = torch.tensor([np.inf, -np.inf, np.nan, 60000, -60000, 30, -30, 0])
+    x, w, ws, xs, b, res = [t.to(DEV) for t in (x, w, ws, xs, b, res)]
+    from oracle import linear
+    for act in ("none", "relu", "gelu", "gelu_tanh", "silu"):
+        y = kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, bias=b, activation=act, residual=res).double().cpu().numpy()
+        assert np.isnan(y[0]).all()
+        if m > 1:
+            assert y[1, 0] == np.inf and np.isnan(y[1, 2])
+            with np.errstate(all="ignore"):
+                want = linear.ACT[act](b[3:8].double().cpu().numpy())
+            assert (np.abs(y[1, 3:8] - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -24).all()
+
+
+def test_types_of_results():
+    x, w, ws, xs, b, res = [t.to(DEV) for t in inputs(3, 16, 64, 1, torch.bfloat16)]
+    assert kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs).dtype == torch.float16
+    assert kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, bias=b).dtype == torch.bfloat16
+    assert kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, residual=res).dtype == torch.bfloat16
+    assert kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, dtype=torch.bfloat16).dtype == torch.bfloat16
+    assert kaio.kaio_linear_w8a8(x[:0], w, ws, x_scale=xs[:0]).shape == (0, 16)
+    assert kaio.kaio_linear_w8a8(x, w[:0], ws[:0], x_scale=xs).shape == (3, 0)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rounded", [True, False])
+def test_repeats_streams_and_graphs(rounded):
+    for m in (1, 5, 40, 100, 300):
+        x, w, ws, xs, b, res = [None if t is None else t.to(DEV) for t in inputs(m, 264, 512, 7, torch.float16, rounded=rounded)]
+        call = lambda **kw: kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, bias=b, activation="silu", residual=res, **kw)
+        ref = call()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            out = call()
+        named = call(stream=side)
+        side.synchronize()
+        assert torch.equal(ref, out) and torch.equal(ref, named)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            call(y=out)
+        for i in range(3):
+            res.mul_(0.5)
+            if not rounded:
+                x.mul_(0.75)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            assert torch.equal(got, call())
+
+
+def test_refusals():
+    x, w, ws, xs, b, res = [t.to(DEV) for t in inputs(4, 32, 64, 1, torch.float16)]
+    ok = dict(x=x, w=w, w_scale=ws, x_scale=xs, bias=b, residual=res)
+    bad = [dict(x=x.half()), dict(x_scale=None), dict(w=w.half()), dict(w=w.t()), dict(w=w[:, :32].contiguous()), dict(w_scale=ws.half()),
+           dict(w_scale=ws[:16]), dict(x_scale=xs[:2]), dict(x_scale=xs.half()), dict(bias=b[:16]), dict(bias=b.bfloat16()), dict(bias=b.float()),
+           dict(residual=res.t()), dict(residual=res.bfloat16(), bias=None, y=res), dict(activation="tanh"), dict(dtype=torch.float32),
+           dict(x=x.cpu()), dict(y=torch.empty(4, 16, dtype=torch.float16, device=DEV)), dict(workspace=torch.empty(8, device=DEV))]
+    for kw in bad:
+        with pytest.raises((TypeError, ValueError)):
+            kaio.kaio_linear_w8a8(**{**ok, **kw})
+    with pytest.raises(kaio.KaioError):                        # y inside x
+        kaio.kaio_linear_w8a8(**{**ok, "y": x.view(-1).view(torch.float16).view(4, 32), "residual": None})
+    with pytest.raises(kaio.KaioError):
+        kaio.kaio_linear_w8a8(torch.zeros(1, 131072, dtype=torch.int8, device=DEV), torch.zeros(1, 131072, dtype=torch.int8, device=DEV),
+                              ws[:1], x_scale=xs[:1])
+    with pytest.raises(kaio.KaioError):                        # too small a workspace
+        kaio.kaio_linear_w8a8(x.half(), w, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        kaio.kaio_linear_w8a8(x[:, :24].contiguous(), w[:, :24].contiguous(), ws, x_scale=xs)

@@ -1,0 +1,194 @@
+"""The mixture-of-experts feed-forward on the GPU against the oracle (tolerance: oracle.moe.moe)."""
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_w4a16_amd as kaio
+from oracle import moe as om
+from tests.gpu_util import DEV, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(e, h, i, seed=0):
+    r = np.random.default_rng(seed)
+    w = lambda k, n: r.integers(0, 2 ** 32, (e, k // 8, n), dtype=np.uint64).astype(np.uint32)
+    s = lambda k, n: r.uniform(0.005, 0.02, (e, k // 128, n)).astype(np.float16)
+    router = (r.standard_normal((e, h)) * 2 / np.sqrt(h)).astype(np.float16)
+    return [router, w(h, i), s(h, i), w(h, i), s(h, i), w(i, h), s(i, h)]
+
+
+def tokens(t, h, seed=0):
+    return np.random.default_rng(seed + 1000).standard_normal((t, h)).astype(np.float16)
+
+
+def compare(y, want, tol):
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"{(~(err <= tol)).sum()} of {err.size} outside tolerance, max ratio {np.nanmax(err / tol):.3f}"
+
+
+def run_case(t, e, top, h, i, normalize=True, act="silu", residual=False, seed=0, in_place=False):
+    ws, x = weights(e, h, i, seed), tokens(t, h, seed)
+    res = tokens(t, h, seed + 1) if residual else None
+    experts = kaio.KaioExperts(*[to_dev(a) for a in ws])
+    dres = None if res is None else to_dev(res)
+    y = dres if in_place else torch.full((t, h), float("nan"), dtype=torch.float16, device=DEV)
+    got = kaio.kaio_moe_w4a16(to_dev(x), experts, top, normalize=normalize, activation=act, residual=dres, y=y)
+    torch.cuda.synchronize()
+    assert got is y
+    compare(got, *om.moe(x, *ws, top, normalize, act, res))
+
+
+@pytest.mark.parametrize("t,e,top,h,i", [
+    (1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (2, 64, 8, 384, 128), (3, 65, 3, 128, 640), (5, 5, 5, 128, 256), (7, 129, 16, 256, 128),
+    (15, 4, 1, 512, 256), (16, 16, 4, 256, 128), (17, 30, 6, 384, 384), (32, 8, 8, 256, 256), (33, 128, 8, 512, 256),
+    (48, 3, 2, 128, 1024), (63, 64, 1, 256, 128), (64, 60, 4, 384, 384), (64, 512, 16, 128, 128), (65, 8, 2, 256, 128),
+    (130, 300, 5, 128, 256), (200, 2, 1, 256, 256)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_sizes(t, e, top, h, i, normalize):
+    run_case(t, e, top, h, i, normalize, residual=t % 2 == 0)
+
+
+@pytest.mark.parametrize("t,e,top,h,i", [(1, 64, 8, 2048, 1024), (4, 8, 2, 4096, 512), (20, 16, 4, 1024, 2048)])
+def test_long_sums(t, e, top, h, i):
+    run_case(t, e, top, h, i, residual=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_activations(act):
+    run_case(6, 8, 2, 256, 256, act=act)
+    run_case(40, 4, 2, 128, 128, act=act, normalize=False, residual=True)
+
+
+@pytest.mark.parametrize("t", [1, 30, 70])
+def test_residual_in_place(t):
+    run_case(t, 8, 2, 256, 128, residual=True, in_place=True)
+
+
+def both(x, ws, top, **kw):
+    y = kaio.kaio_moe_w4a16(to_dev(x), kaio.KaioExperts(*[to_dev(a) for a in ws]), top, **kw)
+    torch.cuda.synchronize()
+    return y, om.moe(x, *ws, top, **kw)
+
+
+@pytest.mark.parametrize("e", [8, 70, 200, 512])
+def test_ties_go_to_the_lowest_expert(e):
+    ws, x = weights(e, 128, 128), tokens(9, 128)
+    ws[0][e // 2:] = ws[0][:e - e // 2]           # every score twice
+    ws[0][3] = ws[0][1]
+    x[4] = 0                                      # all scores alike
+    y, want = both(x, ws, 4)
+    compare(y, *want)
+
+
+@pytest.mark.parametrize("t", [3, 40, 64])
+def test_all_tokens_to_the_same_experts(t):
+    ws, x = weights(16, 128, 256), tokens(t, 128)
+    x[:, 0] = 5
+    ws[0][:, 0] = np.where(np.isin(np.arange(16), (2, 11)), 8, -8)
+    y, want = both(x, ws, 2)
+    compare(y, *want)
+
+
+def test_scores_that_overflow_exp_and_shares_that_vanish():
+    ws, x = weights(32, 256, 128), tokens(10, 256)
+    ws[0] = (ws[0].astype(np.float32) * 300).astype(np.float16)
+    for normalize in (True, False):
+        y, want = both(x, ws, 6, normalize=normalize)
+        compare(y, *want)
+
+
+def test_values_that_are_not_finite_stay_where_they_are():
+    ws, x = weights(16, 256, 128), tokens(20, 256)
+    chosen, _ = om.choose(x, ws[0], 2, True)
+    bad = chosen[7][0]                             # an expert whose scales are not numbers
+    ws[2][bad, 0, 5] = np.nan
+    ws[4][bad, 1, 9] = np.inf
+    ws[6][bad, :, 77] = np.inf
+    free = np.array([bad not in c for c in chosen])
+    x[3, 10], x[11, 0] = np.nan, np.inf            # tokens that are not numbers
+    free[[3, 11]] = False
+    y = kaio.kaio_moe_w4a16(to_dev(x), kaio.KaioExperts(*[to_dev(a) for a in ws]), 2)
+    torch.cuda.synchronize()
+    assert free.sum() > 4 and not free[7]
+    want, tol = om.moe(x[free], *ws, 2)
+    compare(y[torch.from_numpy(free).to(DEV)], want, tol)
+    assert y[3].isnan().any() and y[11].isnan().any() and not y[7].isfinite().all()
+
+
+def test_a_score_that_is_not_a_number_comes_last():
+    ws, x = weights(8, 128, 128), tokens(5, 128)
+    ws[0][2, 7] = np.nan
+    y, want = both(x, ws, 3)
+    assert all(2 not in c for c in om.choose(x, ws[0], 3, True)[0])
+    compare(y, *want)
+
+
+def test_h_that_overflows_is_infinite():
+    ws, x = weights(4, 128, 128), tokens(3, 128)
+    x[1] *= 2000
+    y = kaio.kaio_moe_w4a16(to_dev(x), kaio.KaioExperts(*[to_dev(a) for a in ws]), 1)
+    torch.cuda.synchronize()
+    assert not y[1].isfinite().all()
+    want, tol = om.moe(x[[0, 2]], *ws, 1)
+    compare(y[[0, 2]], want, tol)
+
+
+def test_repeats_streams_graphs_and_shared_workspaces():
+    ws = weights(24, 256, 256)
+    experts = kaio.KaioExperts(*[to_dev(a) for a in ws])
+    for t in (1, 20, 100):
+        x = to_dev(tokens(t, 256))
+        need = kaio.lib().kaio_moe_w4a16_workspace_size(experts._ref, t, 4)
+        scratch = torch.full((need,), 255, dtype=torch.uint8, device=DEV)      # what it holds does not matter
+        ref = kaio.kaio_moe_w4a16(x, experts, 4, residual=x)
+        again = kaio.kaio_moe_w4a16(x, experts, 4, residual=x, workspace=scratch)
+        torch.cuda.synchronize()
+        assert torch.equal(ref, again)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        named = kaio.kaio_moe_w4a16(x, experts, 4, residual=x, stream=side)
+        side.synchronize()
+        assert torch.equal(ref, named)
+        out, graphs = [torch.empty_like(x) for _ in range(2)], []
+        for y, top in zip(out, (4, 2)):            # two graphs, one workspace
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                kaio.kaio_moe_w4a16(x, experts, top, residual=x, y=y, workspace=scratch)
+            graphs.append(g)
+        for _ in range(3):
+            x.copy_(torch.randn_like(x))
+            for g in graphs:
+                g.replay()
+            torch.cuda.synchronize()
+            for y, top in zip(out, (4, 2)):
+                assert torch.equal(y, kaio.kaio_moe_w4a16(x, experts, top, residual=x))
+            torch.cuda.synchronize()
+
+
+def test_empty_and_rows_of_a_larger_tensor():
+    ws = weights(8, 128, 128)
+    experts = kaio.KaioExperts(*[to_dev(a) for a in ws])
+    x = to_dev(tokens(12, 128))
+    assert kaio.kaio_moe_w4a16(x[:0], experts, 2).shape == (0, 128)
+    whole, part = kaio.kaio_moe_w4a16(x, experts, 2), kaio.kaio_moe_w4a16(x[4:9], experts, 2)
+    torch.cuda.synchronize()
+    err = (whole[4:9].double() - part.double()).abs()
+    assert (err <= 2.0 ** -10 * whole[4:9].abs().double() + 1e-3).all()
+
+
+def test_refusals():
+    ws = [to_dev(a) for a in weights(8, 128, 256)]
+    experts, x = kaio.KaioExperts(*ws), to_dev(tokens(4, 128))
+    for kw in (dict(top_k=0), dict(top_k=9), dict(activation="tanh"), dict(residual=x[:2]), dict(y=x.float()), dict(x=x.float()),
+               dict(x=to_dev(tokens(4, 256))), dict(x=x.cpu()), dict(residual=x.bfloat16()), dict(workspace=x), dict(experts=ws)):
+        with pytest.raises((TypeError, ValueError)):
+            kaio.kaio_moe_w4a16(**{**dict(x=x, experts=experts, top_k=2), **kw})
+    with pytest.raises(kaio.KaioError):
+        kaio.kaio_moe_w4a16(x, experts, 2, y=x)
+    with pytest.raises(kaio.KaioError):
+        kaio.kaio_moe_w4a16(x, experts, 2, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    for i, t in enumerate(ws):
+        for other in (t[:4], t.float() if t.dtype != torch.float16 else t.bfloat16(), t.cpu(), t.transpose(0, 1)):
+            with pytest.raises((TypeError, ValueError)):
+                kaio.KaioExperts(*[other if j == i else a for j, a in enumerate(ws)])
