@@ -669,7 +669,7 @@ kaio_status kaio_quantize_rows(kaio_dtype dtype, const void* x, int8_t* q, float
 }
 
 size_t kaio_linear_w8a8_workspace_size(uint32_t m, uint32_t n, uint32_t k, int32_t int8_x) {
-  if (k % 16 != 0 || k > kaio::kLinear8MaxK || m == 0 || n == 0 || int8_x) return 0;
+  if (k % 16 != 0 || k > kaio::kLinear8MaxK || m == 0 || n == 0 || int8_x || kaio::linear8_rounds(m, n, k)) return 0;
   return kaio::linear8_workspace(m, k);
 }
 
@@ -712,6 +712,7 @@ kaio_status kaio_linear_w8a8(kaio_dtype dtype, const void* x, const float* x_sca
   if (kaio_status st = check_device(op)) return st;
   (void)hipGetLastError();
   kaio::Linear8 p;
+  p.x16 = rounds && need == 0 ? static_cast<const uint16_t*>(x) : nullptr;
   p.x = static_cast<const int8_t*>(x);
   p.xs = x_scale;
   p.w = w;
@@ -723,7 +724,7 @@ kaio_status kaio_linear_w8a8(kaio_dtype dtype, const void* x, const float* x_sca
   p.act = act;
   p.bf16 = type == KAIO_DTYPE_BF16;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (rounds) {
+  if (need) {
     uint8_t* const q = static_cast<uint8_t*>(workspace);
     float* const scale = reinterpret_cast<float*>(q + kaio::linear8_rows_bytes(m, k));
     if (hipError_t e = kaio::launch_quantize_rows(static_cast<const uint16_t*>(x), p.bf16, q, scale, m, k, st))

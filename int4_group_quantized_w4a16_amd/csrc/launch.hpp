@@ -215,6 +215,7 @@ hipError_t launch_quantize_rows(const uint16_t* x, bool bf16, uint8_t* q, float*
 
 // y = act(xs ws (x . w^T) + bias) + residual in 8-bit integers; bias and residual may be null.
 struct Linear8 {
+  const uint16_t* x16;        // 16-bit [m, k] to be rounded by the kernel (linear8_rounds), else null, and then
   const int8_t* x;            // [m, k]
   const float* xs;            // [m]
   const int8_t* w;            // [n, k]
@@ -230,8 +231,47 @@ constexpr uint32_t kLinear8MaxK = (1u << 17) - 16;   // |sum| <= 2^14 k stays be
 // bytes of m rounded rows of k, then of their scales
 constexpr uint64_t linear8_rows_bytes(uint64_t m, uint64_t k) { return m * k; }
 constexpr uint64_t linear8_workspace(uint64_t m, uint64_t k) { return linear8_rows_bytes(m, k) + (4 * m + 15) / 16 * 16; }
+// Forms of the 8-bit product: strips of 16 channels by their waves (up to 16 tokens), tiles of channels x tokens.
+enum Linear8Form { kStrip16, kStrip4, kTile32x32, kTile32x64, kTile64x32, kTile64x64, kTile64x128, kTile128x128, kTile128x256, kTile256x256 };
+// Of a tile form the time (0.1 us at k = 4096, n = 4096, weights from HBM) of one workgroup on every compute unit, and of
+// two at once where they fit (0: they do not).  A form's tiles fill the compute units layer by layer, and a layer takes its
+// time however many tiles it has: us at n = 4096 by m = 64 / 96 / 128 / 256 / 384 / 509 / 1024 / 2048: 32x32 8.2 11.3 11.3, 32x64 10.4
+// 9.7 10.4 18.5, 64x64 12.6 12.2 12.6 12.8 18.2 18.9, 64x128 - - - 16.4 16.4 16.5 29.4, 128x128 - - - 20.8 20.8 20.8 21.1
+// 39.9, 128x256 - - - - - - 29.2 33.8, 256x256 - - - - - - - 50.6 (57 of six at 8192 x 12288, 128x256 67.6 there).
+struct Linear8Cost {
+  Linear8Form f;
+  uint32_t channels, tokens, one, two;
+};
+constexpr Linear8Cost kLinear8Forms[] = {
+    {kTile32x32, 32, 32, 82, 113},    {kTile32x64, 32, 64, 104, 0},     {kTile64x32, 64, 32, 110, 0},   {kTile64x64, 64, 64, 126, 187},
+    {kTile64x128, 64, 128, 164, 0}, {kTile128x128, 128, 128, 211, 0}, {kTile128x256, 128, 256, 338, 0}, {kTile256x256, 256, 256, 570, 0}};
+constexpr uint64_t linear8_cost(const Linear8Cost& c, uint64_t m, uint64_t n) {
+  const uint64_t tiles = (m + c.tokens - 1) / c.tokens * ((n + c.channels - 1) / c.channels);
+  const uint64_t layers = (tiles + kComputeUnits - 1) / kComputeUnits;
+  return c.two ? layers / 2 * c.two + layers % 2 * c.one : layers * c.one;
+}
+constexpr Linear8Form linear8_form(uint32_t m, uint32_t n) {
+  // Strips, us with weights from HBM, 16 waves / 4: 16 x 4096 x 4096 6.9 / 7.6, 1 x 11004 x 4096 12.5 / 12.0, 16 tokens there
+  // 15.8 / 14.9; the smallest tile takes 8.2 and 15.5.
+  if (m <= 16) return n > 8192 ? kStrip4 : kStrip16;
+  Linear8Form best = kTile256x256;
+  uint64_t best_cost = ~0ull;
+  for (const Linear8Cost& c : kLinear8Forms) {
+    const uint64_t t = linear8_cost(c, m, n);
+    if (t < best_cost) {
+      best_cost = t;
+      best = c.f;
+    }
+  }
+  return best;
+}
+// Whether a call rounds its 16-bit x in the product's own workgroups, every one all of it, instead of by a launch of its own.
+constexpr uint32_t kLinear8Round = 1u << 16;   // elements of x that they take
+constexpr bool linear8_rounds(uint32_t m, uint32_t n, uint32_t k) {
+  return m <= 16 && linear8_form(m, n) == kStrip16 && (uint64_t)m * k <= kLinear8Round;
+}
 // a bound on the workgroups of a call in any form
-constexpr uint64_t linear8_wgs(uint64_t m, uint64_t n) { return (m + 63) / 64 * ((n + 63) / 64); }
+constexpr uint64_t linear8_wgs(uint64_t m, uint64_t n) { return (m + 31) / 32 * ((n + 15) / 16); }
 hipError_t launch_linear_w8a8(const Linear8& p, hipStream_t stream);
 
 // Mixture of experts.  Tokens are taken in blocks of kMoeBlock, each of which has its own active experts.

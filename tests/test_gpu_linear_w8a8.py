@@ -6,6 +6,7 @@ import torch
 import int4_group_quantized_w4a16_amd as kaio
 from oracle import linear8 as ol
 from tests.gpu_util import DEV
+from tests.linear8_forms import SIZES
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.float16, torch.bfloat16]
@@ -169,6 +170,40 @@ def test_repeats_streams_and_graphs(rounded):
             assert torch.equal(got, call())
 
 
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("dtype,rounded,act,bias,residual", [(TYPES[0], True, "none", False, False), (TYPES[1], False, "gelu_tanh", True, True)])
+def test_every_form(m, n, k, dtype, rounded, act, bias, residual):
+    # (the oracle's arithmetic in float64 on the GPU: whole numbers below 2^53)
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+    w = torch.randint(-128, 128, (n, k), generator=g, device=DEV, dtype=torch.int8)
+    ws = torch.rand(n, generator=g, device=DEV) * 4e-4 + 1e-4
+    if rounded:
+        x, xs = torch.randint(-128, 128, (m, k), generator=g, device=DEV, dtype=torch.int8), torch.rand(m, generator=g, device=DEV) * 0.04 + 0.01
+        xq = x.double()
+    else:
+        x, xs = torch.randn(m, k, generator=g, device=DEV).to(dtype), None
+        most = x.double().abs().amax(1)
+        xq, scale = torch.round(127 * x.double() / most[:, None]), (most / 127).float()
+    b = torch.randn(n, generator=g, device=DEV).to(dtype) if bias else None
+    r = torch.randn(m, n, generator=g, device=DEV).to(dtype) if residual else None
+    y = torch.full((m + 1, n), float("nan"), dtype=dtype, device=DEV)
+    y[m] = 7
+    if rounded:
+        kaio.kaio_linear_w8a8(x, w, ws, x_scale=xs, bias=b, activation=act, residual=r, y=y[:m])
+    else:
+        kaio.kaio_linear_w8a8(x, w, ws, bias=b, activation=act, residual=r, y=y[:m])
+    assert (y[m] == 7).all()                            # the row behind stays as it was
+    p = (xq @ w.double().T.contiguous()) * (xs if rounded else scale).double()[:, None] * ws.double()
+    z = p + b.double() if bias else p
+    a = z / (1 + torch.exp(-2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))) if act == "gelu_tanh" else z
+    want = a + r.double() if residual else a
+    half_step, low = STEP[dtype]
+    tol = half_step * want.abs() + low + 1.13 * 2.0 ** -24 * (4 * p.abs() + (b.double().abs() if bias else 0)) + \
+        2.0 ** -19 * a.abs() * (1 + z.abs() / 32) + 2.0 ** -24 * (a.abs() + (r.double().abs() if residual else 0))
+    err = (y[:m].double() - want).abs()
+    assert (err <= tol).all(), f"{int((~(err <= tol)).sum())} of {err.numel()} outside tolerance"
+
+
 def test_refusals():
     x, w, ws, xs, b, res = [t.to(DEV) for t in inputs(4, 32, 64, 1, torch.float16)]
     ok = dict(x=x, w=w, w_scale=ws, x_scale=xs, bias=b, residual=res)
@@ -185,6 +220,6 @@ def test_refusals():
         kaio.kaio_linear_w8a8(torch.zeros(1, 131072, dtype=torch.int8, device=DEV), torch.zeros(1, 131072, dtype=torch.int8, device=DEV),
                               ws[:1], x_scale=xs[:1])
     with pytest.raises(kaio.KaioError):                        # too small a workspace
-        kaio.kaio_linear_w8a8(x.half(), w, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        kaio.kaio_linear_w8a8(x.half().repeat(10, 1), w, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         kaio.kaio_linear_w8a8(x[:, :24].contiguous(), w[:, :24].contiguous(), ws, x_scale=xs)
