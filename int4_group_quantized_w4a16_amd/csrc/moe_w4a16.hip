@@ -8,8 +8,8 @@
 // weights are the work, each read once:
 //
 // * scores: f64 sums of exact products, so that the order of experts is the
-//   formula's wherever f64 tells them apart; a wave takes one expert and four
-//   tokens.
+//   formula's wherever f64 tells them apart; a workgroup takes one expert and
+//   up to four tokens.
 // * routes: 64 tokens (a block) per workgroup.  A wave finds a token's top_k by
 //   top_k maxima over keys in its registers; every expert's tokens are a mask
 //   of 64 bits, and the experts with any, in order, are the active ones.
@@ -21,6 +21,7 @@
 //   expert's result is added in the same registers.  The parts' sums go to the
 //   workspace in f32, and the last workgroup to arrive adds them in order.
 
+#include "attention_common.hpp"
 #include "common.hpp"
 #include "epilogue.hpp"
 #include "launch.hpp"
@@ -34,16 +35,17 @@ constexpr int kUpWaves = 8, kDownWaves = 8;
 typedef unsigned long long u64;
 
 // ---- scores -----------------------------------------------------------------
-constexpr int kScoreTokens = 4;
+// One expert and kTokens tokens per workgroup.
+template <int kTokens>
 __global__ void __launch_bounds__(256) moe_scores_kernel(Moe p) {
-  const uint32_t lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6), t0 = blockIdx.y * kScoreTokens;
-  if (e >= p.experts) return;
+  __shared__ double part[4][kTokens];
+  const uint32_t tid = threadIdx.x, e = blockIdx.x, t0 = blockIdx.y * kTokens;
   const half8_t* const r = reinterpret_cast<const half8_t*>(p.router + (size_t)e * p.hidden);
-  double sum[kScoreTokens] = {};
-  for (uint32_t c = lane; c < p.hidden / 8; c += 64) {
+  double sum[kTokens] = {};
+  for (uint32_t c = tid; c < p.hidden / 8; c += 256) {
     const half8_t rv = r[c];
 #pragma unroll
-    for (int i = 0; i < kScoreTokens; ++i) {
+    for (int i = 0; i < kTokens; ++i) {
       const uint32_t t = t0 + i < p.tokens ? t0 + i : p.tokens - 1;
       const half8_t xv = reinterpret_cast<const half8_t*>(p.x + (size_t)t * p.hidden)[c];
 #pragma unroll
@@ -51,11 +53,14 @@ __global__ void __launch_bounds__(256) moe_scores_kernel(Moe p) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < kScoreTokens; ++i) {
+  for (int i = 0; i < kTokens; ++i) {
 #pragma unroll
     for (int s = 32; s; s >>= 1) sum[i] += __shfl_xor(sum[i], s);
-    if (lane == 0 && t0 + i < p.tokens) p.scores[(size_t)(t0 + i) * p.experts + e] = sum[i];
+    if (tid % 64 == 0) part[tid / 64][i] = sum[i];
   }
+  __syncthreads();
+  if (tid < kTokens && t0 + tid < p.tokens)
+    p.scores[(size_t)(t0 + tid) * p.experts + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
 }
 
 // ---- routes -----------------------------------------------------------------
@@ -69,17 +74,21 @@ __device__ __forceinline__ u64 key_of(double z) {
 __device__ __forceinline__ double score_of(u64 k) {
   return k == 1 ? (double)NAN : __builtin_bit_cast(double, k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
 }
+// The largest of the wave's values (row shifts, then the rows' last lanes to the next; lane 63 ends with it).
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#pragma unroll
-  for (int s = 32; s; s >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)x, s);
-    x = x > o ? x : o;
-  }
-  return x;
+  auto with = [&](uint32_t o) { x = x > o ? x : o; };
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false));
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false));
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false));
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false));
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));
+  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
 struct RouteShared {
   u64 mask[kMoeMaxExperts];
+  MoeRoute route[kMoeMaxExperts];   // of the active experts
   uint32_t choice[kBlock][kMoeMaxTop];
   float share[kBlock][kMoeMaxTop];
   uint32_t waves[2][16];
@@ -177,17 +186,16 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
     active += a;
   }
   if (tid == 0) p.active[b] = active;
-  if (any) {
-    const size_t a = (size_t)b * p.slots + place - 1;
-    p.route[a] = MoeRoute{mask, tid, rows - count};
-    // (a token chooses an expert once)
-    for (uint32_t t = 0; t < kBlock; ++t) {
-      float share = 0.f;
-      if (mask >> t & 1)
-        for (uint32_t j = 0; j < p.top_k; ++j)
-          if (s.choice[t][j] == tid) share = s.share[t][j];
-      p.share[a * kBlock + t] = share;
-    }
+  const size_t slot0 = (size_t)b * p.slots;
+  if (any) s.route[place - 1] = p.route[slot0 + place - 1] = MoeRoute{mask, tid, rows - count};
+  __syncthreads();
+  for (uint32_t o = tid; o < active * kBlock; o += 1024) {
+    const uint32_t t = o % kBlock;
+    const MoeRoute r = s.route[o / kBlock];
+    float share = 0.f;
+    if (r.mask >> t & 1)   // (a token chooses an expert once)
+      for (uint32_t j = 0; j < p.top_k; ++j) share = s.choice[t][j] == r.expert ? s.share[t][j] : share;
+    p.share[slot0 * kBlock + o] = share;
   }
 }
 
@@ -278,44 +286,62 @@ template <int RT>
 __global__ void __launch_bounds__(kDownWaves * 64) moe_down_kernel(Moe p) {
   __shared__ float part[kDownWaves][16][64];
   __shared__ uint32_t last;
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kq = lane >> 4;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / 64;
   const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * 64, col = n0 + 4 * l16;
   const uint32_t tokens = p.tokens - b * kBlock < kBlock ? p.tokens - b * kBlock : kBlock;
   const u64 units = (u64)p.active[b] * groups;
   const uint32_t u0 = (uint32_t)(units * split / p.splits), u1 = (uint32_t)(units * (split + 1) / p.splits);
-  floatx4 acc[RT][4] = {};
-  for (uint32_t u = u0 + wave; u < u1; u += kDownWaves) {
-    const uint32_t a = u / groups, g = u % groups;
-    const size_t slot = (size_t)b * p.slots + a;
-    const MoeRoute route = p.route[slot];
+  struct Unit {
     Words v;
-    v.load(p.w_down + (size_t)route.expert * (I / 8) * H, p.s_down + (size_t)route.expert * groups * H, H, g, kq, col);
-    const uint16_t* const h = p.h + ((size_t)b * kBlock * p.top_k + route.first) * I + g * kGroup + 8 * kq;
+    MoeRoute route;
+    uint32_t a, g;
+    __device__ __forceinline__ void load(const Moe& p, uint32_t u, uint32_t b, uint32_t groups, uint32_t kq, uint32_t col) {
+      a = u / groups;
+      g = u - a * groups;
+      route = p.route[(size_t)b * p.slots + a];
+      v.load(p.w_down + (size_t)route.expert * (p.inner / 8) * p.hidden, p.s_down + (size_t)route.expert * groups * p.hidden,
+             p.hidden, g, kq, col);
+    }
+  };
+  floatx4 acc[RT][4] = {};
+  auto multiply = [&](const Unit& u) {
+    const uint16_t* const h = p.h + ((size_t)b * kBlock * p.top_k + u.route.first) * I + u.g * kGroup + 8 * kq;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const uint32_t here = (uint32_t)(route.mask >> (16 * r)) & 0xFFFFu;
+      const uint32_t here = (uint32_t)(u.route.mask >> (16 * r)) & 0xFFFFu;
       if (here == 0) continue;
       const uint32_t t = 16 * r + l16;
-      const bool mine = here >> l16 & 1;
       half8_t hv[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         hv[s] = half8_t{};
-        if (mine) hv[s] = *reinterpret_cast<const half8_t*>(h + (size_t)__popcll(route.mask & ((1ull << t) - 1)) * I + 32 * s);
+        if (here >> l16 & 1)
+          hv[s] = *reinterpret_cast<const half8_t*>(h + (size_t)__popcll(u.route.mask & ((1ull << t) - 1)) * I + 32 * s);
       }
-      const floatx4 share = *reinterpret_cast<const floatx4*>(p.share + slot * kBlock + 16 * r + 4 * kq);
+      const floatx4 share = *reinterpret_cast<const floatx4*>(p.share + ((size_t)b * p.slots + u.a) * kBlock + 16 * r + 4 * kq);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         floatx4 c = {};
 #pragma unroll
-        for (int s = 0; s < 4; ++s) c = mfma16x16x32(hv[s], v.operand(s, i), c);
-        const float f = (float)v.s[i] * kUnpackScaledInv;
+        for (int s = 0; s < 4; ++s) c = mfma16x16x32(hv[s], u.v.operand(s, i), c);
+        const float f = (float)u.v.s[i] * kUnpackScaledInv;
         // nothing of an expert that a token did not choose, whatever its scales hold
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[r][i][e] = here >> (4 * kq + e) & 1 ? __builtin_fmaf(c[e] * f, share[e], acc[r][i][e]) : acc[r][i][e];
       }
     }
+  };
+  // the next unit's weights are on the way while one is multiplied
+  Unit even, odd;
+  uint32_t u = u0 + wave;
+  if (u < u1) even.load(p, u, b, groups, kq, col);
+  for (; u < u1; u += 2 * kDownWaves) {
+    if (u + kDownWaves < u1) odd.load(p, u + kDownWaves, b, groups, kq, col);
+    multiply(even);
+    if (u + kDownWaves >= u1) break;
+    if (u + 2 * kDownWaves < u1) even.load(p, u + 2 * kDownWaves, b, groups, kq, col);
+    multiply(odd);
   }
   auto finish = [&](size_t t, uint32_t c, float y) {
     if (p.residual) y += h2f(p.residual[t * H + c]);
@@ -335,22 +361,24 @@ __global__ void __launch_bounds__(kDownWaves * 64) moe_down_kernel(Moe p) {
       for (int w = 0; w < kDownWaves; ++w) y += part[w][o / 64][c];
       const size_t token = (size_t)b * kBlock + t;
       if (p.splits == 1) finish(token, n0 + c, y);
-      else p.partial[((size_t)split * p.tokens + token) * H + n0 + c] = y;
+      else __hip_atomic_store(&p.partial[((size_t)split * p.tokens + token) * H + n0 + c], y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
   }
   if (p.splits == 1) return;
-  // the last of the strip's workgroups adds the parts, in order
-  __threadfence();
+  // The last of the strip's workgroups adds the parts, in order.  Parts are written and read past the L2 of one XCD (relaxed
+  // atomics of the device's scope) and are there once the stores are done: a fence instead would have every workgroup
+  // write back all that its L2 holds (5 times the time of this kernel).
+  wait_vm<0>();
   __syncthreads();
-  if (tid == 0) last = atomicAdd(&p.arrived[(size_t)b * strips + strip], 1u) == p.splits - 1;
+  if (tid == 0) last = __hip_atomic_fetch_add(&p.arrived[(size_t)b * strips + strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   for (uint32_t o = tid; o < tokens * 64; o += kDownWaves * 64) {
     const size_t token = (size_t)b * kBlock + o / 64;
     float y = 0.f;
-    for (uint32_t s = 0; s < p.splits; ++s) y += p.partial[(s * (size_t)p.tokens + token) * H + n0 + o % 64];
+    for (uint32_t s = 0; s < p.splits; ++s)
+      y += __hip_atomic_load(&p.partial[(s * (size_t)p.tokens + token) * H + n0 + o % 64], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     finish(token, n0 + o % 64, y);
   }
 }
@@ -359,8 +387,8 @@ __global__ void __launch_bounds__(kDownWaves * 64) moe_down_kernel(Moe p) {
 
 hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream) {
   const uint32_t blocks = (p.tokens + kBlock - 1) / kBlock;
-  hipLaunchKernelGGL(moe_scores_kernel, dim3((p.experts + 3) / 4, (p.tokens + kScoreTokens - 1) / kScoreTokens), dim3(256), 0,
-                     stream, p);
+  if (p.tokens == 1) hipLaunchKernelGGL(moe_scores_kernel<1>, dim3(p.experts), dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL(moe_scores_kernel<4>, dim3(p.experts, (p.tokens + 3) / 4), dim3(256), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
   if (p.experts <= 64) hipLaunchKernelGGL(moe_routes_kernel<1>, dim3(blocks), dim3(1024), 0, stream, p);
   else if (p.experts <= 128) hipLaunchKernelGGL(moe_routes_kernel<2>, dim3(blocks), dim3(1024), 0, stream, p);
