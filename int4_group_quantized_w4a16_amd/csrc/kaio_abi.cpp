@@ -265,7 +265,8 @@ bool moe_fits(const kaio_experts* e, uint32_t tokens, uint32_t top_k) {
   uint64_t bytes = 0;
   const kaio::MoePlan plan = kaio::moe_plan(tokens, e->experts, e->hidden, e->inner, top_k);
   return bytes_of((uint64_t)e->experts * e->hidden, e->inner, 1, &bytes) && plan.bytes < (1ull << 62) &&
-         plan.slots * (e->inner / 64) <= kaio::kMaxWorkgroups && plan.splits * (e->hidden / 64) <= kaio::kMaxWorkgroups;
+         plan.slots * (e->inner / kaio::kMoeStrip) <= kaio::kMaxWorkgroups &&
+         plan.splits * (e->hidden / kaio::kMoeStrip) <= kaio::kMaxWorkgroups;
 }
 
 // The checks of a paged cache that need no pointers: dtype and sizes.
@@ -804,7 +805,7 @@ kaio_status kaio_moe_w4a16(const kaio_experts* e, const void* x, const void* res
   char* const at = static_cast<char*>(workspace);
   p.scores = reinterpret_cast<double*>(at);
   p.route = reinterpret_cast<kaio::MoeRoute*>(at + plan.route);
-  p.share = reinterpret_cast<float*>(at + plan.share);
+  p.pair = reinterpret_cast<kaio::MoePair*>(at + plan.pair);
   p.active = reinterpret_cast<uint32_t*>(at + plan.active);
   p.arrived = reinterpret_cast<uint32_t*>(at + plan.arrived);
   p.h = reinterpret_cast<uint16_t*>(at + plan.h);

@@ -276,9 +276,13 @@ hipError_t launch_linear_w8a8(const Linear8& p, hipStream_t stream);
 
 // Mixture of experts.  Tokens are taken in blocks of kMoeBlock, each of which has its own active experts.
 constexpr uint32_t kMoeBlock = 64, kMoeMaxExperts = 512, kMoeMaxTop = 16, kMoeMaxTokens = 1u << 17;
-struct MoeRoute {             // an active expert: its tokens (bits of the block), and its first row of h in the block
-  uint64_t mask;
-  uint32_t expert, first;
+constexpr uint32_t kMoeStrip = 32;   // columns of the products' workgroups
+struct MoeRoute {             // an active expert: its rows of h in the block
+  uint32_t expert, first, count;
+};
+struct MoePair {              // a row of h: the token (of the block), and the expert's share of its result
+  uint32_t token;
+  float share;
 };
 struct Moe {
   const uint16_t *x, *router, *residual;        // [tokens, hidden], [experts, hidden], [tokens, hidden] or null
@@ -292,14 +296,14 @@ struct Moe {
   // workspace
   double* scores;             // [tokens, experts]
   MoeRoute* route;            // [blocks, slots]
-  float* share;               // [blocks, slots, kMoeBlock]
-  uint32_t *active, *arrived; // [blocks], [blocks, hidden / 64]
+  MoePair* pair;              // [tokens * top_k]
+  uint32_t *active, *arrived; // [blocks], [blocks, hidden / kMoeStrip]
   uint16_t* h;                // [tokens * top_k, inner]
   float* partial;             // [splits, tokens, hidden] where splits > 1
 };
 struct MoePlan {
   uint64_t blocks, slots, splits;
-  uint64_t route, share, active, arrived, h, partial, bytes;   // offsets in the workspace (scores come first)
+  uint64_t route, pair, active, arrived, h, partial, bytes;   // offsets in the workspace (scores come first)
 };
 constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, uint64_t inner, uint64_t top_k) {
   MoePlan a{};
@@ -307,7 +311,7 @@ constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, u
   const uint64_t pairs = (tokens < kMoeBlock ? tokens : kMoeBlock) * top_k;
   a.slots = pairs < experts ? pairs : experts;
   // two workgroups of the down product per compute unit, of two units for each wave at least
-  const uint64_t strips = hidden / 64 * a.blocks, units = a.slots * (inner / 128);
+  const uint64_t strips = hidden / kMoeStrip * a.blocks, units = a.slots * (inner / 128);
   const uint64_t fill = (2 * kComputeUnits + strips - 1) / strips, most = units / 16 ? units / 16 : 1;
   a.splits = fill < most ? fill : most;
   uint64_t at = 0;
@@ -318,9 +322,9 @@ constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, u
   };
   take(tokens * experts * 8);
   a.route = take(a.blocks * a.slots * sizeof(MoeRoute));
-  a.share = take(a.blocks * a.slots * kMoeBlock * 4);
+  a.pair = take(tokens * top_k * sizeof(MoePair));
   a.active = take(a.blocks * 4);
-  a.arrived = take(a.blocks * (hidden / 64) * 4);
+  a.arrived = take(a.blocks * (hidden / kMoeStrip) * 4);
   a.h = take(tokens * top_k * inner * 2);
   a.partial = take(a.splits > 1 ? a.splits * tokens * hidden * 4 : 0);
   a.bytes = at;

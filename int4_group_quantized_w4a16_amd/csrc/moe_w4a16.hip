@@ -26,6 +26,9 @@
 #include "epilogue.hpp"
 #include "launch.hpp"
 
+#ifndef KAIO_C
+#define KAIO_C 2
+#endif
 namespace kaio {
 namespace {
 
@@ -87,8 +90,8 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 }
 
 struct RouteShared {
-  u64 mask[kMoeMaxExperts];
-  MoeRoute route[kMoeMaxExperts];   // of the active experts
+  u64 mask[kMoeMaxExperts];         // tokens of each expert
+  uint32_t first[kMoeMaxExperts];   // its first row of h
   uint32_t choice[kBlock][kMoeMaxTop];
   float share[kBlock][kMoeMaxTop];
   uint32_t waves[2][16];
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x, t0 = b * kBlock;
   const uint32_t tokens = p.tokens - t0 < kBlock ? p.tokens - t0 : kBlock;
   if (tid < kMoeMaxExperts) s.mask[tid] = 0;
-  for (uint32_t i = tid; i < p.hidden / 64; i += 1024) p.arrived[(size_t)b * (p.hidden / 64) + i] = 0;
+  for (uint32_t i = tid; i < p.hidden / kMoeStrip; i += 1024) p.arrived[(size_t)b * (p.hidden / kMoeStrip) + i] = 0;
   __syncthreads();
   for (uint32_t t = wave; t < tokens; t += 16) choose<V>(p, s, t, t0 + t, lane);
   __syncthreads();
@@ -186,184 +189,253 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
     active += a;
   }
   if (tid == 0) p.active[b] = active;
-  const size_t slot0 = (size_t)b * p.slots;
-  if (any) s.route[place - 1] = p.route[slot0 + place - 1] = MoeRoute{mask, tid, rows - count};
+  if (any) {
+    p.route[(size_t)b * p.slots + place - 1] = MoeRoute{tid, rows - count, count};
+    s.first[tid] = rows - count;
+  }
   __syncthreads();
-  for (uint32_t o = tid; o < active * kBlock; o += 1024) {
-    const uint32_t t = o % kBlock;
-    const MoeRoute r = s.route[o / kBlock];
-    float share = 0.f;
-    if (r.mask >> t & 1)   // (a token chooses an expert once)
-      for (uint32_t j = 0; j < p.top_k; ++j) share = s.choice[t][j] == r.expert ? s.share[t][j] : share;
-    p.share[slot0 * kBlock + o] = share;
+  MoePair* const pairs = p.pair + (size_t)b * kBlock * p.top_k;
+  for (uint32_t o = tid; o < tokens * p.top_k; o += 1024) {
+    const uint32_t t = o / p.top_k, j = o % p.top_k, e = s.choice[t][j];
+    pairs[s.first[e] + __popcll(s.mask[e] & ((1ull << t) - 1))] = MoePair{t, s.share[t][j]};
   }
 }
 
 // ---- products ---------------------------------------------------------------
-// A lane's four words of a 32-k step: row (lane / 16) of the step's four, columns 4 (lane % 16) .. + 3 of the strip;
-// word i is then the B operand of the MFMA whose column c stands for column 4c + i.
+// A lane's C words of each of a group's four 32-k steps: row (lane / 16) of the step's four, columns C (lane % 16) .. + C - 1
+// of the strip; word i is then the B operand of the MFMA whose column c stands for column C c + i.
+template <int C>
 struct Words {
-  uint4 w[4];
-  half4_t s;
+  static_assert(C == 2 || C == 4, "columns of a lane");
+  typedef uint32_t Row __attribute__((ext_vector_type(C)));
+  typedef _Float16 Scales __attribute__((ext_vector_type(C)));
+  Row w[4];
+  Scales s;
+  // of group g, wave-uniform as the bases; the lane's part of an address fits in 32 bits
   __device__ __forceinline__ void load(const uint32_t* w_, const uint16_t* s_, uint32_t n, uint32_t g, uint32_t kq, uint32_t col) {
+    const uint32_t lane = kq * n + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(w_ + (size_t)(g * 16 + i * 4 + kq) * n + col);
-    s = *reinterpret_cast<const half4_t*>(s_ + (size_t)g * n + col);
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const Row*>(w_ + (size_t)(g * 16 + i * 4) * n + lane);
+    s = *reinterpret_cast<const Scales*>(s_ + (size_t)g * n + col);
   }
-  __device__ __forceinline__ half8_t operand(int step, int i) const {
-    const uint4& v = w[step];
-    return unpack_int4x8_scaled(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
-  }
+  __device__ __forceinline__ half8_t operand(int step, int i) const { return unpack_int4x8_scaled(w[step][i]); }
+  __device__ __forceinline__ float scale(int i) const { return (float)s[i] * kUnpackScaledInv; }
 };
 
-// 64 columns of act(x G) * (x U) for the tokens of one active expert
-__global__ void __launch_bounds__(kUpWaves * 64) moe_up_kernel(Moe p) {
-  __shared__ float part[kUpWaves][2][16][64];
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kq = lane >> 4;
-  const uint32_t b = blockIdx.y, strips = p.inner / 64, a = blockIdx.x / strips, n0 = blockIdx.x % strips * 64;
+// 16 C columns of act(x G) * (x U) for the tokens of one active expert, 16 RT of them at a time
+template <int C, int RT>
+__global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(Moe p) {
+  constexpr uint32_t N = 16 * C;
+  __shared__ float part[kUpWaves][2][16][N];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
+  const uint32_t b = blockIdx.y, strips = p.inner / N, a = blockIdx.x / strips, n0 = blockIdx.x % strips * N;
   if (a >= p.active[b]) return;
   const MoeRoute route = p.route[(size_t)b * p.slots + a];
-  const uint32_t rows = __popcll(route.mask), col = n0 + 4 * l16;
-  const uint32_t H = p.hidden, I = p.inner;
-  const size_t wat = (size_t)route.expert * (H / 8) * I, sat = (size_t)route.expert * (H / kGroup) * I;
+  const uint32_t col = n0 + C * l16, H = p.hidden, I = p.inner, groups = H / kGroup;
+  const size_t wat = (size_t)route.expert * (H / 8) * I, sat = (size_t)route.expert * groups * I;
   const uint32_t *wg = p.w_gate + wat, *wu = p.w_up + wat;
   const uint16_t *sg = p.s_gate + sat, *su = p.s_up + sat;
-  for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
-    // the token of this lane's row: the (r0 + l16)-th bit of the mask
-    u64 left = route.mask;
-    const uint32_t skip = r0 + l16 < rows ? r0 + l16 : rows - 1;
-    for (uint32_t i = 0; i < skip; ++i) left &= left - 1;
-    const uint16_t* const x = p.x + ((size_t)b * kBlock + __builtin_ctzll(left)) * H + 8 * kq;
-    floatx4 gate[4] = {}, up[4] = {};
-    for (uint32_t g = wave; g < H / kGroup; g += kUpWaves) {
-      Words vg, vu;
-      half8_t xv[4];
-      vg.load(wg, sg, I, g, kq, col);
-      vu.load(wu, su, I, g, kq, col);
+  const MoePair* const pairs = p.pair + (size_t)b * kBlock * p.top_k + route.first;
+  struct Group {
+    Words<C> gate, up;
+  } ahead;
+  auto load = [&](Group& v, uint32_t g) {
+    v.gate.load(wg, sg, I, g, kq, col);
+    v.up.load(wu, su, I, g, kq, col);
+  };
+  for (uint32_t r0 = 0; r0 < route.count; r0 += 16 * RT) {
+    if (wave < groups) load(ahead, wave);
+    const uint16_t* x[RT];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) xv[s] = *reinterpret_cast<const half8_t*>(x + g * kGroup + 32 * s);
+    for (int r = 0; r < RT; ++r) {   // past the last row that one
+      const uint32_t row = r0 + 16 * r + l16;
+      x[r] = p.x + ((size_t)b * kBlock + pairs[row < route.count ? row : route.count - 1].token) * H + 8 * kq;
+    }
+    floatx4 gate[RT][C] = {}, up[RT][C] = {};
+    auto multiply = [&](const Group& v, uint32_t g) {
+      half8_t xv[RT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        floatx4 cg = {}, cu = {};
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          cg = mfma16x16x32(xv[s], vg.operand(s, i), cg);
-          cu = mfma16x16x32(xv[s], vu.operand(s, i), cu);
-        }
-        const float fg = (float)vg.s[i] * kUnpackScaledInv, fu = (float)vu.s[i] * kUnpackScaledInv;
+        for (int s = 0; s < 4; ++s) xv[r][s] = *reinterpret_cast<const half8_t*>(x[r] + g * kGroup + 32 * s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          gate[i][e] = __builtin_fmaf(cg[e], fg, gate[i][e]);
-          up[i][e] = __builtin_fmaf(cu[e], fu, up[i][e]);
+      for (int i = 0; i < C; ++i) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          const Words<C>& w = which ? v.up : v.gate;
+          // one column set's operands at a time: unpacked ahead they take more registers than there are
+          __builtin_amdgcn_sched_barrier(0);
+          half8_t o[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) o[s] = w.operand(s, i);
+          const float f = w.scale(i);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            if (r && r0 + 16 * r >= route.count) break;
+            floatx4 c = {};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) c = mfma16x16x32(xv[r][s], o[s], c);
+            floatx4& sum = which ? up[r][i] : gate[r][i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(c[e], f, sum[e]);
+          }
         }
       }
+    };
+    // the next group's weights are on the way while one is multiplied
+#pragma unroll 1
+    for (uint32_t g = wave; g < groups; g += kUpWaves) {
+      const Group now = ahead;
+      if (g + kUpWaves < groups) load(ahead, g + kUpWaves);
+      multiply(now, g);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      *reinterpret_cast<floatx4*>(&part[wave][0][4 * kq + e][4 * l16]) = floatx4{gate[0][e], gate[1][e], gate[2][e], gate[3][e]};
-      *reinterpret_cast<floatx4*>(&part[wave][1][4 * kq + e][4 * l16]) = floatx4{up[0][e], up[1][e], up[2][e], up[3][e]};
-    }
-    __syncthreads();
-    for (uint32_t o = tid; o < 16 * 64; o += kUpWaves * 64) {
-      const uint32_t r = o / 64, c = o % 64;
-      if (r0 + r >= rows) break;
-      float y[1] = {0.f}, z = 0.f;
+    for (int r = 0; r < RT; ++r) {
+      if (r0 + 16 * r >= route.count) break;
 #pragma unroll
-      for (int w = 0; w < kUpWaves; ++w) {
-        y[0] += part[w][0][r][c];
-        z += part[w][1][r][c];
+      for (int e = 0; e < 4; ++e) {
+        typedef float Columns __attribute__((ext_vector_type(C)));
+        Columns vg, vu;
+#pragma unroll
+        for (int i = 0; i < C; ++i) vg[i] = gate[r][i][e], vu[i] = up[r][i][e];
+        *reinterpret_cast<Columns*>(&part[wave][0][4 * kq + e][C * l16]) = vg;
+        *reinterpret_cast<Columns*>(&part[wave][1][4 * kq + e][C * l16]) = vu;
       }
-      activations<1>(y, p.act);
-      // rounded to f16, as the next product's other operand
-      p.h[((size_t)b * kBlock * p.top_k + route.first + r0 + r) * I + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)(y[0] * z));
+      __syncthreads();
+      for (uint32_t o = tid; o < 16 * N; o += kUpWaves * 64) {
+        const uint32_t row = r0 + 16 * r + o / N, c = o % N;
+        if (row >= route.count) break;
+        float y[1] = {0.f}, z = 0.f;
+#pragma unroll
+        for (int w = 0; w < kUpWaves; ++w) {
+          y[0] += part[w][0][o / N][c];
+          z += part[w][1][o / N][c];
+        }
+        activations<1>(y, p.act);
+        // rounded to f16, as the next product's other operand
+        p.h[((size_t)b * kBlock * p.top_k + route.first + row) * I + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)(y[0] * z));
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
-// 64 hidden columns of one part of the (active expert, group) units, for RT tiles of 16 tokens
-template <int RT>
-__global__ void __launch_bounds__(kDownWaves * 64) moe_down_kernel(Moe p) {
-  __shared__ float part[kDownWaves][16][64];
+// 16 C hidden columns of one part of the (active expert, group) units.  A wave takes consecutive ones and adds an expert's
+// result, times the shares, to sums of its own in LDS, [token][column]; the waves' sums are added at the end.
+template <int C, int RT>
+__global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_kernel(Moe p) {
+  constexpr uint32_t N = 16 * C;
+  typedef float Columns __attribute__((ext_vector_type(C)));
+  extern __shared__ __attribute__((aligned(16))) float sums[];   // [wave][tokens of the block][N]
+  __shared__ MoeRoute routes[kMoeMaxExperts];
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
-  const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / 64;
-  const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * 64, col = n0 + 4 * l16;
+  const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / N;
+  const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * N, col = n0 + C * l16;
   const uint32_t tokens = p.tokens - b * kBlock < kBlock ? p.tokens - b * kBlock : kBlock;
   const u64 units = (u64)p.active[b] * groups;
-  const uint32_t u0 = (uint32_t)(units * split / p.splits), u1 = (uint32_t)(units * (split + 1) / p.splits);
+  const uint32_t u0 = (uint32_t)(units * split / p.splits), u1 = (uint32_t)(units * (split + 1) / p.splits), n = u1 - u0;
+  const uint32_t a0 = u0 / groups, wu0 = u0 + n * wave / kDownWaves, wu1 = u0 + n * (wave + 1) / kDownWaves;
+  for (uint32_t i = tid; i * groups + a0 * groups < u1; i += kDownWaves * 64) routes[i] = p.route[(size_t)b * p.slots + a0 + i];
+  float* const mine = sums + wave * tokens * N;
+  for (uint32_t i = lane; i < tokens * N / 4; i += 64) reinterpret_cast<floatx4*>(mine)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  const MoePair* const pairs = p.pair + (size_t)b * kBlock * p.top_k;
+  const uint16_t* const h0 = p.h + (size_t)b * kBlock * p.top_k * I + 8 * kq;
   struct Unit {
-    Words v;
-    MoeRoute route;
-    uint32_t a, g;
-    __device__ __forceinline__ void load(const Moe& p, uint32_t u, uint32_t b, uint32_t groups, uint32_t kq, uint32_t col) {
-      a = u / groups;
-      g = u - a * groups;
-      route = p.route[(size_t)b * p.slots + a];
-      v.load(p.w_down + (size_t)route.expert * (p.inner / 8) * p.hidden, p.s_down + (size_t)route.expert * groups * p.hidden,
-             p.hidden, g, kq, col);
-    }
-  };
-  floatx4 acc[RT][4] = {};
-  auto multiply = [&](const Unit& u) {
-    const uint16_t* const h = p.h + ((size_t)b * kBlock * p.top_k + u.route.first) * I + u.g * kGroup + 8 * kq;
+    Words<C> v;
+    uint32_t a, g;   // the expert's place in routes, and the group
+  } ahead;
+  // rows r0 .. of every expert (a second pass only where an expert has more than 16 RT tokens of the block)
+  for (uint32_t r0 = 0; r0 < tokens; r0 += 16 * RT) {
+    auto seek = [&](uint32_t u) {   // the first unit from u on whose expert has such rows
+      while (u < wu1 && r0 >= routes[u / groups - a0].count) u = (u / groups + 1) * groups;
+      return u < wu1 ? u : wu1;
+    };
+    auto load = [&](Unit& t, uint32_t u) {
+      t.a = __builtin_amdgcn_readfirstlane(u / groups - a0);
+      t.g = __builtin_amdgcn_readfirstlane(u % groups);
+      const size_t e = __builtin_amdgcn_readfirstlane(routes[t.a].expert);
+      t.v.load(p.w_down + e * (I / 8) * H, p.s_down + e * groups * H, H, t.g, kq, col);
+    };
+    floatx4 acc[RT][C] = {};
+    uint32_t expert = ~0u;   // whose rows acc holds
+    auto flush = [&] {
+      if (expert == ~0u) return;
+      const MoeRoute route = routes[expert];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const uint32_t here = (uint32_t)(u.route.mask >> (16 * r)) & 0xFFFFu;
-      if (here == 0) continue;
-      const uint32_t t = 16 * r + l16;
-      half8_t hv[4];
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t row = r0 + 16 * r + 4 * kq;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        hv[s] = half8_t{};
-        if (here >> l16 & 1)
-          hv[s] = *reinterpret_cast<const half8_t*>(h + (size_t)__popcll(u.route.mask & ((1ull << t) - 1)) * I + 32 * s);
+        for (int e = 0; e < 4; ++e) {
+          if (row + e < route.count) {
+            const MoePair pair = pairs[route.first + row + e];
+            Columns* const to = reinterpret_cast<Columns*>(mine + pair.token * N + C * l16);
+            Columns y = *to;
+#pragma unroll
+            for (int i = 0; i < C; ++i) y[i] = __builtin_fmaf(acc[r][i][e], pair.share, y[i]);
+            *to = y;
+          }
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[r][i][e] = 0.f;
+        }
       }
-      const floatx4 share = *reinterpret_cast<const floatx4*>(p.share + ((size_t)b * p.slots + u.a) * kBlock + 16 * r + 4 * kq);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        floatx4 c = {};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) c = mfma16x16x32(hv[s], u.v.operand(s, i), c);
-        const float f = (float)u.v.s[i] * kUnpackScaledInv;
-        // nothing of an expert that a token did not choose, whatever its scales hold
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[r][i][e] = here >> (4 * kq + e) & 1 ? __builtin_fmaf(c[e] * f, share[e], acc[r][i][e]) : acc[r][i][e];
+    };
+    auto multiply = [&](const Unit& t) {
+      if (t.a != expert) {
+        flush();
+        expert = t.a;
       }
+      const uint32_t first = routes[t.a].first, count = routes[t.a].count;
+      half8_t hv[RT][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {   // past the last row that one, whose results go nowhere
+        const uint32_t row = r0 + 16 * r + l16;
+        const uint16_t* const h = h0 + (size_t)(first + (row < count ? row : count - 1)) * I + t.g * kGroup;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) hv[r][s] = *reinterpret_cast<const half8_t*>(h + 32 * s);
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        __builtin_amdgcn_sched_barrier(0);   // (as above)
+        half8_t w[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w[s] = t.v.operand(s, i);
+        const float f = t.v.scale(i);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          floatx4 c = {};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) c = mfma16x16x32(hv[r][s], w[s], c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][i][e] = __builtin_fmaf(c[e], f, acc[r][i][e]);
+        }
+      }
+    };
+    // the next unit's weights are on the way while one is multiplied
+    uint32_t u = seek(wu0);
+    if (u < wu1) load(ahead, u);
+#pragma unroll 1
+    while (u < wu1) {
+      const Unit now = ahead;
+      u = seek(u + 1);
+      if (u < wu1) load(ahead, u);
+      multiply(now);
     }
-  };
-  // the next unit's weights are on the way while one is multiplied
-  Unit even, odd;
-  uint32_t u = u0 + wave;
-  if (u < u1) even.load(p, u, b, groups, kq, col);
-  for (; u < u1; u += 2 * kDownWaves) {
-    if (u + kDownWaves < u1) odd.load(p, u + kDownWaves, b, groups, kq, col);
-    multiply(even);
-    if (u + kDownWaves >= u1) break;
-    if (u + 2 * kDownWaves < u1) even.load(p, u + 2 * kDownWaves, b, groups, kq, col);
-    multiply(odd);
+    flush();
   }
-  auto finish = [&](size_t t, uint32_t c, float y) {
-    if (p.residual) y += h2f(p.residual[t * H + c]);
-    p.y[t * H + c] = __builtin_bit_cast(uint16_t, (_Float16)y);
+  __syncthreads();
+  auto finish = [&](size_t at, float y) {
+    if (p.residual) y += h2f(p.residual[at]);
+    p.y[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
   };
+  for (uint32_t o = tid; o < tokens * N; o += kDownWaves * 64) {
+    float y = 0.f;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<floatx4*>(&part[wave][4 * kq + e][4 * l16]) = floatx4{acc[r][0][e], acc[r][1][e], acc[r][2][e], acc[r][3][e]};
-    __syncthreads();
-    for (uint32_t o = tid; o < 16 * 64; o += kDownWaves * 64) {
-      const uint32_t t = 16 * r + o / 64, c = o % 64;
-      if (t >= tokens) break;
-      float y = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDownWaves; ++w) y += part[w][o / 64][c];
-      const size_t token = (size_t)b * kBlock + t;
-      if (p.splits == 1) finish(token, n0 + c, y);
-      else __hip_atomic_store(&p.partial[((size_t)split * p.tokens + token) * H + n0 + c], y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
+    for (int w = 0; w < kDownWaves; ++w) y += sums[w * tokens * N + o];
+    const size_t at = ((size_t)b * kBlock + o / N) * H + n0 + o % N;
+    if (p.splits == 1) finish(at, y);
+    else __hip_atomic_store(&p.partial[(size_t)split * p.tokens * H + at], y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   if (p.splits == 1) return;
   // The last of the strip's workgroups adds the parts, in order.  Parts are written and read past the L2 of one XCD (relaxed
@@ -374,13 +446,26 @@ __global__ void __launch_bounds__(kDownWaves * 64) moe_down_kernel(Moe p) {
   if (tid == 0) last = __hip_atomic_fetch_add(&p.arrived[(size_t)b * strips + strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
   __syncthreads();
   if (!last) return;
-  for (uint32_t o = tid; o < tokens * 64; o += kDownWaves * 64) {
-    const size_t token = (size_t)b * kBlock + o / 64;
+  for (uint32_t o = tid; o < tokens * N; o += kDownWaves * 64) {
+    const size_t at = ((size_t)b * kBlock + o / N) * H + n0 + o % N;
     float y = 0.f;
     for (uint32_t s = 0; s < p.splits; ++s)
-      y += __hip_atomic_load(&p.partial[(s * (size_t)p.tokens + token) * H + n0 + o % 64], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    finish(token, n0 + o % 64, y);
+      y += __hip_atomic_load(&p.partial[(size_t)s * p.tokens * H + at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    finish(at, y);
   }
+}
+
+template <int RT>
+hipError_t launch_products(const Moe& p, uint32_t blocks, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_up_kernel<KAIO_C, RT>), dim3(p.inner / (16 * KAIO_C) * p.slots, blocks), dim3(kUpWaves * 64), 0, stream, p);
+  if (hipError_t e = hipGetLastError()) return e;
+  auto* kern = &moe_down_kernel<KAIO_C, RT>;
+  const uint32_t tokens = p.tokens < kBlock ? p.tokens : kBlock;
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kDownWaves * kBlock * 16 * KAIO_C * 4);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kern, dim3(p.hidden / (16 * KAIO_C) * p.splits, blocks), dim3(kDownWaves * 64), kDownWaves * tokens * 16 * KAIO_C * 4, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -395,15 +480,7 @@ hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream) {
   else if (p.experts <= 256) hipLaunchKernelGGL(moe_routes_kernel<4>, dim3(blocks), dim3(1024), 0, stream, p);
   else hipLaunchKernelGGL(moe_routes_kernel<8>, dim3(blocks), dim3(1024), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(moe_up_kernel, dim3(p.inner / 64 * p.slots, blocks), dim3(kUpWaves * 64), 0, stream, p);
-  if (hipError_t e = hipGetLastError()) return e;
-  const dim3 grid(p.hidden / 64 * p.splits, blocks);
-  const uint32_t tiles = p.tokens >= kBlock ? 4 : (p.tokens + 15) / 16;
-  if (tiles == 1) hipLaunchKernelGGL(moe_down_kernel<1>, grid, dim3(kDownWaves * 64), 0, stream, p);
-  else if (tiles == 2) hipLaunchKernelGGL(moe_down_kernel<2>, grid, dim3(kDownWaves * 64), 0, stream, p);
-  else if (tiles == 3) hipLaunchKernelGGL(moe_down_kernel<3>, grid, dim3(kDownWaves * 64), 0, stream, p);
-  else hipLaunchKernelGGL(moe_down_kernel<4>, grid, dim3(kDownWaves * 64), 0, stream, p);
-  return hipGetLastError();
+  return launch_products<1>(p, blocks, stream);
 }
 
 }  // namespace kaio
