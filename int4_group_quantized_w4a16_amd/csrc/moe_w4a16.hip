@@ -33,7 +33,8 @@ namespace kaio {
 namespace {
 
 constexpr uint32_t kBlock = kMoeBlock;   // tokens of a block (bits of a mask)
-constexpr int kUpWaves = 8, kDownWaves = 8;
+constexpr int kDownWaves = 8;
+constexpr int kUpAhead = 1, kDownAhead = 3;   // groups' weights on the way to a wave
 
 typedef unsigned long long u64;
 
@@ -211,22 +212,30 @@ struct Words {
   typedef _Float16 Scales __attribute__((ext_vector_type(C)));
   Row w[4];
   Scales s;
-  // of group g, wave-uniform as the bases; the lane's part of an address fits in 32 bits
-  __device__ __forceinline__ void load(const uint32_t* w_, const uint16_t* s_, uint32_t n, uint32_t g, uint32_t kq, uint32_t col) {
-    const uint32_t lane = kq * n + col;
+  // Of group g (wave-uniform as the bases); there: whether there is one.  Loads are issued all the same, of an empty buffer:
+  // under a branch, the compiler's waits for older loads would have to wait for these too.
+  __device__ __forceinline__ void load(const uint32_t* w_, const uint16_t* s_, uint32_t n, uint32_t g, uint32_t kq, uint32_t col,
+                                       bool there) {
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(w_ + (size_t)g * 16 * n), 0, there ? 64 * n : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(s_ + (size_t)g * n), 0, there ? 2 * n : 0, 0x00020000);
+    const uint32_t lane = (kq * n + col) * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const Row*>(w_ + (size_t)(g * 16 + i * 4) * n + lane);
-    s = *reinterpret_cast<const Scales*>(s_ + (size_t)g * n + col);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (C == 2) w[i] = __builtin_bit_cast(Row, __builtin_amdgcn_raw_buffer_load_b64(rw, lane, i * 16 * n, 0));
+      else w[i] = __builtin_bit_cast(Row, __builtin_amdgcn_raw_buffer_load_b128(rw, lane, i * 16 * n, 0));
+    }
+    if constexpr (C == 2) s = __builtin_bit_cast(Scales, __builtin_amdgcn_raw_buffer_load_b32(rs, col * 2, 0, 0));
+    else s = __builtin_bit_cast(Scales, __builtin_amdgcn_raw_buffer_load_b64(rs, col * 2, 0, 0));
   }
   __device__ __forceinline__ half8_t operand(int step, int i) const { return unpack_int4x8_scaled(w[step][i]); }
   __device__ __forceinline__ float scale(int i) const { return (float)s[i] * kUnpackScaledInv; }
 };
 
 // 16 C columns of act(x G) * (x U) for the tokens of one active expert, 16 RT of them at a time
-template <int C, int RT>
-__global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(Moe p) {
+template <int C, int RT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, RT == 1 ? 4 : 2) moe_up_kernel(Moe p) {
   constexpr uint32_t N = 16 * C;
-  __shared__ float part[kUpWaves][2][16][N];
+  __shared__ float part[WAVES][2][16][N];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const uint32_t b = blockIdx.y, strips = p.inner / N, a = blockIdx.x / strips, n0 = blockIdx.x % strips * N;
   if (a >= p.active[b]) return;
@@ -238,13 +247,15 @@ __global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(
   const MoePair* const pairs = p.pair + (size_t)b * kBlock * p.top_k + route.first;
   struct Group {
     Words<C> gate, up;
-  } ahead;
+  };
+  struct Rows {
+    half8_t v[RT][4];
+  };
   auto load = [&](Group& v, uint32_t g) {
-    v.gate.load(wg, sg, I, g, kq, col);
-    v.up.load(wu, su, I, g, kq, col);
+    v.gate.load(wg, sg, I, g, kq, col, g < groups);
+    v.up.load(wu, su, I, g, kq, col, g < groups);
   };
   for (uint32_t r0 = 0; r0 < route.count; r0 += 16 * RT) {
-    if (wave < groups) load(ahead, wave);
     const uint16_t* x[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {   // past the last row that one
@@ -252,12 +263,14 @@ __global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(
       x[r] = p.x + ((size_t)b * kBlock + pairs[row < route.count ? row : route.count - 1].token) * H + 8 * kq;
     }
     floatx4 gate[RT][C] = {}, up[RT][C] = {};
-    auto multiply = [&](const Group& v, uint32_t g) {
-      half8_t xv[RT][4];
+    auto read = [&](Rows& v, uint32_t g) {   // past the last group that one
+      const uint32_t at = (g < groups ? g : groups - 1) * kGroup;
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) xv[r][s] = *reinterpret_cast<const half8_t*>(x[r] + g * kGroup + 32 * s);
+        for (int s = 0; s < 4; ++s) v.v[r][s] = *reinterpret_cast<const half8_t*>(x[r] + at + 32 * s);
+    };
+    auto multiply = [&](const Group& v, const Rows& rows) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
 #pragma unroll
@@ -274,20 +287,31 @@ __global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(
             if (r && r0 + 16 * r >= route.count) break;
             floatx4 c = {};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) c = mfma16x16x32(xv[r][s], o[s], c);
+            for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[r][s], o[s], c);
             floatx4& sum = which ? up[r][i] : gate[r][i];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(c[e], f, sum[e]);
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
-    // the next group's weights are on the way while one is multiplied
+    // Loads come back in order.  kUpAhead groups' weights are on the way while one is multiplied, and the rows that the next
+    // one needs are asked for before the last of them.
+    Group ahead[kUpAhead];
+    Rows rows;
+    read(rows, wave);
+#pragma unroll
+    for (int j = 0; j < kUpAhead; ++j) load(ahead[j], wave + j * WAVES);
 #pragma unroll 1
-    for (uint32_t g = wave; g < groups; g += kUpWaves) {
-      const Group now = ahead;
-      if (g + kUpWaves < groups) load(ahead, g + kUpWaves);
-      multiply(now, g);
+    for (uint32_t g = wave; g < groups; g += WAVES) {
+      const Group now = ahead[0];
+      const Rows with = rows;
+#pragma unroll
+      for (int j = 0; j + 1 < kUpAhead; ++j) ahead[j] = ahead[j + 1];
+      read(rows, g + WAVES);
+      load(ahead[kUpAhead - 1], g + kUpAhead * WAVES);
+      multiply(now, with);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -302,12 +326,12 @@ __global__ void __launch_bounds__(kUpWaves * 64, RT == 1 ? 4 : 2) moe_up_kernel(
         *reinterpret_cast<Columns*>(&part[wave][1][4 * kq + e][C * l16]) = vu;
       }
       __syncthreads();
-      for (uint32_t o = tid; o < 16 * N; o += kUpWaves * 64) {
+      for (uint32_t o = tid; o < 16 * N; o += WAVES * 64) {
         const uint32_t row = r0 + 16 * r + o / N, c = o % N;
         if (row >= route.count) break;
         float y[1] = {0.f}, z = 0.f;
 #pragma unroll
-        for (int w = 0; w < kUpWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
           y[0] += part[w][0][o / N][c];
           z += part[w][1][o / N][c];
         }
@@ -327,7 +351,8 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
   constexpr uint32_t N = 16 * C;
   typedef float Columns __attribute__((ext_vector_type(C)));
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [wave][tokens of the block][N]
-  __shared__ MoeRoute routes[kMoeMaxExperts];
+  __shared__ MoeRoute routes[kMoeMaxExperts];            // of the experts of this part
+  __shared__ MoePair pairs[kBlock * kMoeMaxTop];         // and their rows
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / N;
@@ -340,23 +365,51 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
   float* const mine = sums + wave * tokens * N;
   for (uint32_t i = lane; i < tokens * N / 4; i += 64) reinterpret_cast<floatx4*>(mine)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
-  const MoePair* const pairs = p.pair + (size_t)b * kBlock * p.top_k;
+  const uint32_t row0 = routes[0].first;
+  if (n) {
+    const MoeRoute end = routes[(u1 - 1) / groups - a0];
+    for (uint32_t i = tid; i < end.first + end.count - row0; i += kDownWaves * 64) pairs[i] = p.pair[(size_t)b * kBlock * p.top_k + row0 + i];
+  }
+  __syncthreads();
   const uint16_t* const h0 = p.h + (size_t)b * kBlock * p.top_k * I + 8 * kq;
-  struct Unit {
-    Words<C> v;
-    uint32_t a, g;   // the expert's place in routes, and the group
-  } ahead;
+  struct Rows {
+    half8_t v[RT][4];
+  };
   // rows r0 .. of every expert (a second pass only where an expert has more than 16 RT tokens of the block)
   for (uint32_t r0 = 0; r0 < tokens; r0 += 16 * RT) {
-    auto seek = [&](uint32_t u) {   // the first unit from u on whose expert has such rows
-      while (u < wu1 && r0 >= routes[u / groups - a0].count) u = (u / groups + 1) * groups;
-      return u < wu1 ? u : wu1;
+    // the wave's units whose expert has such rows, one after the other; past the last that one, and not there
+    struct Unit {
+      uint32_t u, a, g;   // the unit, its expert's place in routes, its group
+      bool there;
     };
-    auto load = [&](Unit& t, uint32_t u) {
-      t.a = __builtin_amdgcn_readfirstlane(u / groups - a0);
-      t.g = __builtin_amdgcn_readfirstlane(u % groups);
+    auto settle = [&](Unit t) {
+      while (t.there && r0 >= routes[t.a].count) {   // on to the next expert
+        t.u += groups - t.g;
+        ++t.a;
+        t.g = 0;
+        t.there = t.u < wu1;
+      }
+      return t;
+    };
+    auto after = [&](const Unit& t) {
+      if (t.u + 1 >= wu1) return Unit{t.u, t.a, t.g, false};
+      const bool same = t.g + 1 < groups;
+      const Unit n = settle(Unit{t.u + 1, same ? t.a : t.a + 1, same ? t.g + 1 : 0, true});
+      return n.there ? n : Unit{t.u, t.a, t.g, false};
+    };
+    auto load = [&](Words<C>& v, const Unit& t) {
       const size_t e = __builtin_amdgcn_readfirstlane(routes[t.a].expert);
-      t.v.load(p.w_down + e * (I / 8) * H, p.s_down + e * groups * H, H, t.g, kq, col);
+      v.load(p.w_down + e * (I / 8) * H, p.s_down + e * groups * H, H, t.g, kq, col, t.there);
+    };
+    auto read = [&](Rows& v, const Unit& t) {   // past the last row that one, whose results go nowhere
+      const uint32_t first = routes[t.a].first, count = routes[t.a].count;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t row = r0 + 16 * r + l16;
+        const uint16_t* const h = h0 + (size_t)(first + (row < count ? row : count - 1)) * I + t.g * kGroup;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v.v[r][s] = *reinterpret_cast<const half8_t*>(h + 32 * s);
+      }
     };
     floatx4 acc[RT][C] = {};
     uint32_t expert = ~0u;   // whose rows acc holds
@@ -369,7 +422,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (row + e < route.count) {
-            const MoePair pair = pairs[route.first + row + e];
+            const MoePair pair = pairs[route.first - row0 + row + e];
             Columns* const to = reinterpret_cast<Columns*>(mine + pair.token * N + C * l16);
             Columns y = *to;
 #pragma unroll
@@ -381,46 +434,58 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
         }
       }
     };
-    auto multiply = [&](const Unit& t) {
-      if (t.a != expert) {
+    auto multiply = [&](const Words<C>& v, const Rows& rows, uint32_t a) {
+      if (a != expert) {
         flush();
-        expert = t.a;
-      }
-      const uint32_t first = routes[t.a].first, count = routes[t.a].count;
-      half8_t hv[RT][4];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {   // past the last row that one, whose results go nowhere
-        const uint32_t row = r0 + 16 * r + l16;
-        const uint16_t* const h = h0 + (size_t)(first + (row < count ? row : count - 1)) * I + t.g * kGroup;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) hv[r][s] = *reinterpret_cast<const half8_t*>(h + 32 * s);
+        expert = a;
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         __builtin_amdgcn_sched_barrier(0);   // (as above)
         half8_t w[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) w[s] = t.v.operand(s, i);
-        const float f = t.v.scale(i);
+        for (int s = 0; s < 4; ++s) w[s] = v.operand(s, i);
+        const float f = v.scale(i);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           floatx4 c = {};
 #pragma unroll
-          for (int s = 0; s < 4; ++s) c = mfma16x16x32(hv[r][s], w[s], c);
+          for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[r][s], w[s], c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[r][i][e] = __builtin_fmaf(c[e], f, acc[r][i][e]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
-    // the next unit's weights are on the way while one is multiplied
-    uint32_t u = seek(wu0);
-    if (u < wu1) load(ahead, u);
+    if (wu0 >= wu1) break;
+    Unit t = settle(Unit{wu0, wu0 / groups - a0, wu0 % groups, true});
+    if (!t.there) continue;
+    // Weights and rows ahead of their use as in the product before.
+    Words<C> ahead[kDownAhead];
+    Unit next = after(t), second = after(next), furthest = t;
+    Rows rows, rows_next;
+    read(rows, t);
+    read(rows_next, next);
+#pragma unroll
+    for (int j = 0; j < kDownAhead; ++j) {
+      load(ahead[j], furthest);
+      if (j + 1 < kDownAhead) furthest = after(furthest);
+    }
 #pragma unroll 1
-    while (u < wu1) {
-      const Unit now = ahead;
-      u = seek(u + 1);
-      if (u < wu1) load(ahead, u);
-      multiply(now);
+    for (;;) {
+      const Words<C> now = ahead[0];
+      const Rows with = rows;
+#pragma unroll
+      for (int j = 0; j + 1 < kDownAhead; ++j) ahead[j] = ahead[j + 1];
+      rows = rows_next;
+      read(rows_next, second);
+      furthest = after(furthest);
+      load(ahead[kDownAhead - 1], furthest);
+      multiply(now, with, t.a);
+      if (!next.there) break;
+      t = next;
+      next = second;
+      second = after(second);
     }
     flush();
   }
@@ -457,7 +522,9 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
 
 template <int RT>
 hipError_t launch_products(const Moe& p, uint32_t blocks, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_up_kernel<KAIO_C, RT>), dim3(p.inner / (16 * KAIO_C) * p.slots, blocks), dim3(kUpWaves * 64), 0, stream, p);
+  const uint32_t wgs = p.inner / (16 * KAIO_C) * p.slots;
+  if ((uint64_t)wgs * blocks <= 4 * kComputeUnits) hipLaunchKernelGGL((moe_up_kernel<KAIO_C, RT, 8>), dim3(wgs, blocks), dim3(8 * 64), 0, stream, p);
+  else hipLaunchKernelGGL((moe_up_kernel<KAIO_C, RT, 4>), dim3(wgs, blocks), dim3(4 * 64), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
   auto* kern = &moe_down_kernel<KAIO_C, RT>;
   const uint32_t tokens = p.tokens < kBlock ? p.tokens : kBlock;
