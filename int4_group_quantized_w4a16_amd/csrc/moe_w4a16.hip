@@ -10,8 +10,8 @@
 // * scores: f64 sums of exact products, so that the order of experts is the
 //   formula's wherever f64 tells them apart; a workgroup takes one expert and
 //   up to four tokens.
-// * routes: 64 tokens (a block) per workgroup.  A wave finds a token's top_k by
-//   top_k maxima over keys in its registers; every expert's tokens are a mask
+// * routes: 64 tokens (a block) per workgroup.  16 lanes find a token's top_k by
+//   top_k maxima over keys in their registers; every expert's tokens are a mask
 //   of 64 bits, and the experts with any, in order, are the active ones.
 // * up: one workgroup per active expert and 64 inner columns; its waves share
 //   out the groups along the hidden axis, 16 of the expert's tokens at a time.
@@ -78,17 +78,16 @@ __device__ __forceinline__ u64 key_of(double z) {
 __device__ __forceinline__ double score_of(u64 k) {
   return k == 1 ? (double)NAN : __builtin_bit_cast(double, k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
 }
-// The largest of the wave's values (row shifts, then the rows' last lanes to the next; lane 63 ends with it).
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-  auto with = [&](uint32_t o) { x = x > o ? x : o; };
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false));
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false));
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false));
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false));
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));
-  with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));
-  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+// The largest and the smallest of the 16 values of a row of lanes, in each of them (rotations within the row).
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  auto with = [&](int o) { x = x > (uint32_t)o ? x : (uint32_t)o; };
+  with(__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, false));
+  with(__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, false));
+  return x;
 }
+__device__ __forceinline__ uint32_t row_min(uint32_t x) { return ~row_max(~x); }
 
 struct RouteShared {
   u64 mask[kMoeMaxExperts];         // tokens of each expert
@@ -98,18 +97,20 @@ struct RouteShared {
   uint32_t waves[2][16];
 };
 
-// the top_k of token t (of the block): V keys per lane, expert lane * V + v
+// The top_k of the block's tokens, 16 lanes each, by top_k maxima; V keys per lane, those of experts lane * V + v.  (A wave
+// for each token, its maxima by way of scalar registers, took 0.2 us for each: 9.7 us in all for 33 tokens and top_k 8.)
 template <int V>
-__device__ __forceinline__ void choose(const Moe& p, RouteShared& s, uint32_t t, size_t token, uint32_t lane) {
+__device__ __forceinline__ void choose(const Moe& p, RouteShared& s, uint32_t t0, uint32_t tokens) {
+  const uint32_t t = threadIdx.x / 16, lane = threadIdx.x % 16;
+  const double* const scores = p.scores + (size_t)(t0 + (t < tokens ? t : 0)) * p.experts;
   u64 key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const uint32_t e = lane * V + v;
-    key[v] = e < p.experts ? key_of(p.scores[token * p.experts + e]) : 0;
+    key[v] = e < p.experts ? key_of(scores[e]) : 0;
   }
-  double top = 0;
-  float sum = 0.f, mine = 0.f;
-  uint32_t chosen = 0;
+  u64 mine = 0, first = 0;   // lane j: the key of the j-th best; and the first's
+  uint32_t chosen = 0;       // and its expert
   for (uint32_t j = 0; j < p.top_k; ++j) {
     u64 best = key[0];
     uint32_t at = 0;
@@ -119,35 +120,29 @@ __device__ __forceinline__ void choose(const Moe& p, RouteShared& s, uint32_t t,
         best = key[v];
         at = v;
       }
-    const uint32_t hi = wave_max((uint32_t)(best >> 32));
-    const bool first = (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = wave_max(first ? (uint32_t)best : 0u);
-    const int l = __builtin_ctzll(__ballot(first && (uint32_t)best == lo));   // ties: the lowest lane, the lowest expert
-    const uint32_t v0 = __builtin_amdgcn_readlane(at, l);
+    const uint32_t hi = row_max((uint32_t)(best >> 32));
+    const uint32_t lo = row_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    const u64 top = (u64)hi << 32 | lo;
+    const uint32_t e = row_min(best == top ? lane * V + at : ~0u);   // ties: the lowest expert
+    if (j == 0) first = top;
+    mine = lane == j ? top : mine;
+    chosen = lane == j ? e : chosen;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane == (uint32_t)l && v0 == (uint32_t)v) key[v] = 0;
-    const double z = score_of((u64)hi << 32 | lo);
-    if (j == 0) {
-      top = z;
-      if (!p.normalize) {   // all of them; the best's own is added with the chosen below
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (key[v]) sum += __expf((float)(score_of(key[v]) - top));
-#pragma unroll
-        for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-      }
-    }
-    const float part = __expf((float)(z - top));
-    if (p.normalize || j == 0) sum += part;
-    if (lane == j) {
-      mine = part;
-      chosen = l * V + v0;
-    }
+    for (int v = 0; v < V; ++v) key[v] = e == lane * V + v ? 0 : key[v];
   }
-  if (lane < p.top_k) {
+  const double top = score_of(first);
+  auto part = [&](u64 k) { return __expf((float)(score_of(k) - top)); };
+  const float own = lane < p.top_k ? part(mine) : 0.f;
+  float sum = own;
+  if (!p.normalize) {   // those that were not chosen
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum += key[v] ? part(key[v]) : 0.f;
+  }
+#pragma unroll
+  for (int x = 8; x; x >>= 1) sum += __shfl_xor(sum, x);
+  if (t < tokens && lane < p.top_k) {
     s.choice[t][lane] = chosen;
-    s.share[t][lane] = mine / sum;
+    s.share[t][lane] = own / sum;
     atomicOr(&s.mask[chosen], 1ull << t);
   }
 }
@@ -161,7 +156,7 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
   if (tid < kMoeMaxExperts) s.mask[tid] = 0;
   for (uint32_t i = tid; i < p.hidden / kMoeStrip; i += 1024) p.arrived[(size_t)b * (p.hidden / kMoeStrip) + i] = 0;
   __syncthreads();
-  for (uint32_t t = wave; t < tokens; t += 16) choose<V>(p, s, t, t0 + t, lane);
+  if (wave * 4 < tokens) choose<V>(p, s, t0, tokens);
   __syncthreads();
   // places of the active experts and of their tokens
   const u64 mask = tid < kMoeMaxExperts ? s.mask[tid] : 0;
@@ -490,33 +485,50 @@ __global__ void __launch_bounds__(kDownWaves * 64, RT == 1 ? 4 : 2) moe_down_ker
     flush();
   }
   __syncthreads();
-  auto finish = [&](size_t at, float y) {
-    if (p.residual) y += h2f(p.residual[at]);
-    p.y[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
-  };
-  for (uint32_t o = tid; o < tokens * N; o += kDownWaves * 64) {
-    float y = 0.f;
+  // four columns of a token at a time
+  const size_t first = (size_t)b * kBlock * H + n0;   // the block's first token
+  auto finish = [&](uint32_t off, floatx4 y) {
+    const size_t at = first + off;
+    half4_t out;
+    half4_t r = {};
+    if (p.residual) r = *reinterpret_cast<const half4_t*>(p.residual + at);
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) y += sums[w * tokens * N + o];
-    const size_t at = ((size_t)b * kBlock + o / N) * H + n0 + o % N;
-    if (p.splits == 1) finish(at, y);
-    else __hip_atomic_store(&p.partial[(size_t)split * p.tokens * H + at], y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int e = 0; e < 4; ++e) out[e] = (_Float16)(y[e] + (float)r[e]);
+    *reinterpret_cast<half4_t*>(p.y + at) = out;
+  };
+  // Parts are written and read past the L2 of one XCD (scope bits of the device, 17) and are there once the stores are done: a
+  // fence instead would have every workgroup write back all that its L2 holds (5 times the time of this kernel).
+  constexpr int kDevice = 17;
+  auto part = [&](uint32_t s) {
+    return __builtin_amdgcn_make_buffer_rsrc(p.partial + (size_t)s * p.tokens * H + first, 0, 0xFFFFFFFFu, 0x00020000);
+  };
+  for (uint32_t o = tid; o < tokens * (N / 4); o += kDownWaves * 64) {
+    floatx4 y = reinterpret_cast<const floatx4*>(sums)[o];
+#pragma unroll
+    for (int w = 1; w < kDownWaves; ++w) y += reinterpret_cast<const floatx4*>(sums + w * tokens * N)[o];
+    const uint32_t off = o / (N / 4) * H + o % (N / 4) * 4;
+    if (p.splits == 1) finish(off, y);
+    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), part(split), off * 4, 0, kDevice);
   }
   if (p.splits == 1) return;
-  // The last of the strip's workgroups adds the parts, in order.  Parts are written and read past the L2 of one XCD (relaxed
-  // atomics of the device's scope) and are there once the stores are done: a fence instead would have every workgroup
-  // write back all that its L2 holds (5 times the time of this kernel).
+  // the last of the strip's workgroups adds the parts, in order
   wait_vm<0>();
   __syncthreads();
   if (tid == 0) last = __hip_atomic_fetch_add(&p.arrived[(size_t)b * strips + strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
   __syncthreads();
   if (!last) return;
-  for (uint32_t o = tid; o < tokens * N; o += kDownWaves * 64) {
-    const size_t at = ((size_t)b * kBlock + o / N) * H + n0 + o % N;
-    float y = 0.f;
-    for (uint32_t s = 0; s < p.splits; ++s)
-      y += __hip_atomic_load(&p.partial[(size_t)s * p.tokens * H + at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    finish(at, y);
+  for (uint32_t o = tid; o < tokens * (N / 4); o += kDownWaves * 64) {
+    const uint32_t off = o / (N / 4) * H + o % (N / 4) * 4;
+    floatx4 y = {};
+    for (uint32_t s0 = 0; s0 < p.splits; s0 += 8) {   // eight loads at a time
+      u32x4 v[8];
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(part(s0 + i < p.splits ? s0 + i : s0), off * 4, 0, kDevice);
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i)
+        if (s0 + i < p.splits) y += __builtin_bit_cast(floatx4, v[i]);
+    }
+    finish(off, y);
   }
 }
 
@@ -542,10 +554,10 @@ hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream) {
   if (p.tokens == 1) hipLaunchKernelGGL(moe_scores_kernel<1>, dim3(p.experts), dim3(256), 0, stream, p);
   else hipLaunchKernelGGL(moe_scores_kernel<4>, dim3(p.experts, (p.tokens + 3) / 4), dim3(256), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
-  if (p.experts <= 64) hipLaunchKernelGGL(moe_routes_kernel<1>, dim3(blocks), dim3(1024), 0, stream, p);
-  else if (p.experts <= 128) hipLaunchKernelGGL(moe_routes_kernel<2>, dim3(blocks), dim3(1024), 0, stream, p);
-  else if (p.experts <= 256) hipLaunchKernelGGL(moe_routes_kernel<4>, dim3(blocks), dim3(1024), 0, stream, p);
-  else hipLaunchKernelGGL(moe_routes_kernel<8>, dim3(blocks), dim3(1024), 0, stream, p);
+  if (p.experts <= 64) hipLaunchKernelGGL(moe_routes_kernel<4>, dim3(blocks), dim3(1024), 0, stream, p);
+  else if (p.experts <= 128) hipLaunchKernelGGL(moe_routes_kernel<8>, dim3(blocks), dim3(1024), 0, stream, p);
+  else if (p.experts <= 256) hipLaunchKernelGGL(moe_routes_kernel<16>, dim3(blocks), dim3(1024), 0, stream, p);
+  else hipLaunchKernelGGL(moe_routes_kernel<32>, dim3(blocks), dim3(1024), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
   return launch_products<1>(p, blocks, stream);
 }
