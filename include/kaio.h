@@ -15,7 +15,8 @@
  *   kaio_quantize_rows      rows of 16-bit numbers rounded to 8 bits
  *   kaio_linear_w8a8        product in 8-bit integers with scales for each
  *                           token and channel, and the same epilogue (two
- *                           launches where it rounds x)
+ *                           launches where more than a few tokens of 16-bit
+ *                           x are to be rounded)
  *   kaio_moe_w4a16          mixture-of-experts feed-forward on W4A16 weights
  *                           (four launches)
  *   kaio_rope_append        rotary positions on Q and K, K and V written to a

@@ -265,11 +265,15 @@ constexpr Linear8Form linear8_form(uint32_t m, uint32_t n) {
   }
   return best;
 }
-// Whether a call rounds its 16-bit x in the product's own workgroups, every one all of it, instead of by a launch of its own.
-constexpr uint32_t kLinear8Round = 1u << 16;   // elements of x that they take
+// Whether a call rounds its 16-bit x in the product's own workgroups, every one all of it, instead of by a launch of its own:
+// us, inside / apart, at m = 1, 4, 8, 16: n 2048, k 2048 5.7 / 5.9, 5.8 / 6.1, 6.3 / 6.5, 7.6 / 6.7; n 4096, k 4096 8.0 / 9.4, 8.5 /
+// 9.7, 9.6 / 9.9, 12.6 / 10.9; n 4096, k 8192 11.4 / 13.6, 13.1 / 14.2, 16.0 / 14.4.  With more than one workgroup for each
+// compute unit it is the other way: n 8192, k 4096 14.0 / 12.7, 15.2 / 13.0, 17.5 / 14.5; 11004 channels 24.4 / 14.7.
+constexpr uint32_t kLinear8Round = 1u << 15;   // elements of x that they take
 constexpr bool linear8_rounds(uint32_t m, uint32_t n, uint32_t k) {
-  return m <= 16 && linear8_form(m, n) == kStrip16 && (uint64_t)m * k <= kLinear8Round;
+  return m <= 8 && n <= 16 * kComputeUnits && (uint64_t)m * k <= kLinear8Round;
 }
+static_assert(linear8_form(8, 16 * kComputeUnits) == kStrip16, "the form that rounds");
 // a bound on the workgroups of a call in any form
 constexpr uint64_t linear8_wgs(uint64_t m, uint64_t n) { return (m + 31) / 32 * ((n + 15) / 16); }
 hipError_t launch_linear_w8a8(const Linear8& p, hipStream_t stream);

@@ -15,7 +15,19 @@
 //
 // Strips (linear8_strip_kernel), few tokens: the weights are the work and go
 // from memory to registers once; a workgroup's waves share out k and add up in
-// LDS.
+// LDS.  Up to 8 tokens are rounded there too (linear8_rounds).
+//
+// Bound: up to some 100 tokens by the weights' way from HBM, 1 byte each; where
+// there are a few thousand rows on both sides by the matrix cores, and at 8192 x
+// 12288 by the power that the card allows them (2.4 to 2.5e15 operations/s in
+// long runs; MFMAs alone without loads reach 3.0 to 3.4e15).  In between a
+// compute unit waits for its own blocks.  Measured (16-bit x, rounding included;
+// m x n x k): 1 x 4096 x 4096 6.2 us (2.7 TB/s), 61 x 11004 x 4096 14.1 (3.3
+// TB/s), 509 x 4096 x 4096 22.7, of which rounding 5, 2048 x 4096 x 8192 77, of
+// which rounding 10 (tiles 2.0e15 operations/s), 8192 x 12288 x 4096 325.
+//
+// Results leave by nontemporal stores (plain ones: 413 instead of 381 us for the
+// last of these, in an earlier form), so that they push no operands out of the L2.
 
 #include "attention_common.hpp"
 #include "common.hpp"
@@ -392,7 +404,7 @@ __device__ __forceinline__ void meet_lds() {
   asm volatile("" ::: "memory");
 }
 
-// The rounded rows of up to 16 tokens in LDS, rows of p.k bytes and zeros to the next multiple of 128, `stride` apart, with
+// The rounded rows of up to 8 tokens in LDS, rows of p.k bytes and zeros to the next multiple of 128, `stride` apart, with
 // their scales.  Made from 16-bit rows by the whole workgroup, kHeld pieces of 16 elements per thread at a time.
 template <bool kBf16, int kThreads, int kHeld>
 struct RoundedRows {
@@ -553,7 +565,7 @@ hipError_t launch_strip(const Linear8& p, hipStream_t stream) {
     hipLaunchKernelGGL(kern, dim3((p.n + 15) / 16), dim3(64 * WAVES), lds, stream, p);
     return hipGetLastError();
   };
-  constexpr int most = (int)(kLinear8Round + 16 * (128 + 16));
+  constexpr int most = (int)(kLinear8Round + 8 * (128 + 16));
   if (p.bf16) {
     auto* kern = &linear8_strip_kernel<kRounds, true, WAVES, kAhead>;
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, most);

@@ -5,7 +5,7 @@ workgroup for the forms that do so.  tests/test_linear8_forms_host.py holds the 
 """
 SIZES = [
     # strips of 16 channels, 16 waves and 4; of 16-bit tokens rounded in the product's workgroups and before it
-    (1, 1000, 384), (16, 1003, 528), (7, 4100, 2064), (16, 520, 4096), (16, 520, 4112), (2, 8200, 400), (16, 8201, 1024),
+    (1, 1000, 384), (16, 1003, 528), (7, 4100, 2064), (16, 520, 4096), (8, 520, 4096), (8, 520, 4112), (3, 4001, 2064), (2, 8200, 400), (16, 8201, 1024),
     # 32 x 32, 32 x 64, 64 x 32, 64 x 64, 64 x 128 (channels x tokens): sets of waves
     (17, 200, 128), (40, 1000, 400), (61, 2048, 256), (96, 4096, 128), (120, 4001, 400), (512, 1024, 640), (24, 11004, 128),
     (32, 10000, 272), (61, 11004, 256), (250, 4096, 400), (1000, 1000, 1008), (128, 11004, 128), (384, 4001, 400),
