@@ -25,7 +25,7 @@ def check(x):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,k", [(1, 16), (3, 32), (4, 1024), (5, 1008), (7, 1040), (2, 4096), (9, 4112), (3, 8192), (2, 8208), (3, 16384),
-                                 (2, 16400), (1, 40000), (1000, 48), (257, 2064)])
+                                 (2, 16400), (2, 32768), (1, 32784), (1, 40000), (1000, 48), (257, 2064)])
 def test_sizes(dtype, m, k):
     g = torch.Generator().manual_seed(m + k)
     check((torch.randn(m, k, generator=g) * torch.rand(m, 1, generator=g) * 4).to(dtype))
