@@ -12,7 +12,7 @@
 // * scores: f64 sums of exact products, so that the order of experts is the
 //   formula's wherever f64 tells them apart; a workgroup takes one expert and
 //   up to four tokens.
-// * routes: a block per workgroup.  16 lanes find a token's top_k by top_k
+// * routes: a block per workgroup (a wave for a token alone).  16 lanes find a token's top_k by top_k
 //   maxima over keys in their registers; every expert's tokens are a mask of 64
 //   bits, and the experts with any, in order, are the active ones.  An active
 //   expert's rows are consecutive, so that h holds no empty ones.
@@ -28,7 +28,7 @@
 //
 // Measured, in us, scores + routes + up + down; E experts of I inner and H hidden
 // columns, the active ones' weights over the last two: 1 token, E 64, top 8, I
-// 1024, H 2048: 3 + 5 + 8 + 9 (latency: one wait for memory each).  8 tokens, E 8,
+// 1024, H 2048: 3 + 3 + 8 + 8 (latency: one wait for memory each).  8 tokens, E 8,
 // top 2, I 8192, H 4096: 5 + 4 + 49 + 36 (374 MB, 4.4 TB/s).  33 tokens, E 128, top
 // 8, I 768, H 2048: 6 + 8 + 41 + 31 (274 MB, 3.8 TB/s).  64 tokens, E 60, top 4, I
 // 1408, H 2048: 6 + 6 + 40 + 31 (262 MB, 3.7 TB/s).  A copy reaches 5.2 TB/s.
@@ -106,12 +106,17 @@ struct RouteShared {
   uint32_t waves[2][16];
 };
 
-// The top_k of the block's tokens, 16 lanes each, by top_k maxima; V keys per lane, those of experts lane * V + v.  (A wave
-// for each token, its maxima by way of scalar registers, took 0.2 us for each: 9.7 us in all for 33 tokens and top_k 8.)
+// The top_k of a token by 16 lanes, by top_k maxima; V keys per lane, those of experts lane * V + v.  Lane j < top_k gets the j-th
+// best and its share.  (A wave for each token, its maxima by way of scalar registers, took 0.2 us for each: 9.7 us in all for
+// 33 tokens and top_k 8.)
+struct Choice {
+  uint32_t expert;
+  float share;
+};
 template <int V>
-__device__ __forceinline__ void choose(const Moe& p, RouteShared& s, uint32_t t0, uint32_t tokens) {
-  const uint32_t t = threadIdx.x / 16, lane = threadIdx.x % 16;
-  const double* const scores = p.scores + (size_t)(t0 + (t < tokens ? t : 0)) * p.experts;
+__device__ __forceinline__ Choice choose(const Moe& p, uint32_t token) {
+  const uint32_t lane = threadIdx.x % 16;
+  const double* const scores = p.scores + (size_t)token * p.experts;
   u64 key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -149,10 +154,19 @@ __device__ __forceinline__ void choose(const Moe& p, RouteShared& s, uint32_t t0
   }
 #pragma unroll
   for (int x = 8; x; x >>= 1) sum += __shfl_xor(sum, x);
-  if (t < tokens && lane < p.top_k) {
-    s.choice[t][lane] = chosen;
-    s.share[t][lane] = own / sum;
-    atomicOr(&s.mask[chosen], 1ull << t);
+  return Choice{chosen, own / sum};
+}
+
+// One token: its choices are the active experts, in order of score.  (By the workgroup below: 4.9 us, here 3.2.)
+template <int V>
+__global__ void __launch_bounds__(64) moe_route_kernel(Moe p) {
+  const uint32_t lane = threadIdx.x;
+  for (uint32_t i = lane; i < p.hidden / kMoeStrip; i += 64) p.arrived[i] = 0;
+  if (lane == 0) p.active[0] = p.top_k;
+  const Choice c = choose<V>(p, 0);
+  if (lane < p.top_k) {
+    p.route[lane] = MoeRoute{c.expert, lane, 1};
+    p.pair[lane] = MoePair{0, c.share};
   }
 }
 
@@ -165,7 +179,15 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
   if (tid < kMoeMaxExperts) s.mask[tid] = 0;
   for (uint32_t i = tid; i < p.hidden / kMoeStrip; i += 1024) p.arrived[(size_t)b * (p.hidden / kMoeStrip) + i] = 0;
   __syncthreads();
-  if (wave * 4 < tokens) choose<V>(p, s, t0, tokens);
+  if (wave * 4 < tokens) {
+    const uint32_t t = tid / 16, j = tid % 16;
+    const Choice c = choose<V>(p, t0 + (t < tokens ? t : 0));
+    if (t < tokens && j < p.top_k) {
+      s.choice[t][j] = c.expert;
+      s.share[t][j] = c.share;
+      atomicOr(&s.mask[c.expert], 1ull << t);
+    }
+  }
   __syncthreads();
   // places of the active experts and of their tokens
   const u64 mask = tid < kMoeMaxExperts ? s.mask[tid] : 0;
@@ -246,8 +268,10 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
   __shared__ float part[WAVES][2][16][N];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const uint32_t b = blockIdx.y, strips = p.inner / N, a = blockIdx.x / strips, n0 = blockIdx.x % strips * N;
-  if (a >= p.active[b]) return;
-  const MoeRoute route = p.route[(size_t)b * p.slots + a];
+  const MoeRoute route = p.route[(size_t)b * p.slots + a];   // whatever it is past the active ones
+  const uint32_t active = p.active[b];
+  asm volatile("" ::"s"(active), "s"(route.expert), "s"(route.first), "s"(route.count));   // both loads on the way at once
+  if (a >= active) return;
   const uint32_t col = n0 + C * l16, H = p.hidden, I = p.inner, groups = H / kGroup;
   const size_t wat = (size_t)route.expert * (H / 8) * I, sat = (size_t)route.expert * groups * I;
   const uint32_t *wg = p.w_gate + wat, *wu = p.w_up + wat;
@@ -261,6 +285,8 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
     v.up.load(wu, su, I, g, kq, col, g < groups);
   };
   for (uint32_t r0 = 0; r0 < route.count; r0 += 16) {
+    Group ahead;
+    load(ahead, wave);   // (the first ones before their rows are known)
     const uint32_t row = r0 + l16 < route.count ? r0 + l16 : route.count - 1;   // past the last that one
     const uint16_t* const x = p.x + ((size_t)b * kBlock + pairs[row].token) * H + 8 * kq;
     floatx4 gate[C] = {}, up[C] = {};
@@ -290,10 +316,8 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
       __builtin_amdgcn_sched_barrier(0);
     };
     // Loads come back in order: the next group's rows and then its weights are on the way while one is multiplied.
-    Group ahead;
     Rows rows;
     read(rows, wave);
-    load(ahead, wave);
 #pragma unroll 1
     for (uint32_t g = wave; g < groups; g += WAVES) {
       const Group now = ahead;
@@ -332,25 +356,23 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
 // result, times the shares, to sums of its own in LDS, [token][column]; the waves' sums are added at the end.
 __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [wave][tokens of the block][N]
-  __shared__ MoeRoute routes[kMoeMaxExperts];            // of the experts of this part
+  __shared__ MoeRoute routes[kMoeMaxExperts];            // of the block's active experts
   __shared__ MoePair pairs[kBlock * kMoeMaxTop];         // and their rows
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / N;
   const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * N, col = n0 + C * l16;
   const uint32_t tokens = p.tokens - b * kBlock < kBlock ? p.tokens - b * kBlock : kBlock;
-  const u64 units = (u64)p.active[b] * groups;
+  // All of them at once, whichever this part needs, and before the number of active ones is known (past it the workspace holds
+  // anything): one wait for memory instead of three.
+  const uint32_t active = p.active[b];   // (first: after stores the compiler would load it by vectors)
+  for (uint32_t i = tid; i < p.slots; i += kDownWaves * 64) routes[i] = p.route[(size_t)b * p.slots + i];
+  for (uint32_t i = tid; i < tokens * p.top_k; i += kDownWaves * 64) pairs[i] = p.pair[(size_t)b * kBlock * p.top_k + i];
+  const u64 units = (u64)active * groups;
   const uint32_t u0 = (uint32_t)(units * split / p.splits), u1 = (uint32_t)(units * (split + 1) / p.splits), n = u1 - u0;
-  const uint32_t a0 = u0 / groups, wu0 = u0 + n * wave / kDownWaves, wu1 = u0 + n * (wave + 1) / kDownWaves;
-  for (uint32_t i = tid; i * groups + a0 * groups < u1; i += kDownWaves * 64) routes[i] = p.route[(size_t)b * p.slots + a0 + i];
+  const uint32_t wu0 = u0 + n * wave / kDownWaves, wu1 = u0 + n * (wave + 1) / kDownWaves;
   float* const mine = sums + wave * tokens * N;
   for (uint32_t i = lane; i < tokens * N / 4; i += 64) reinterpret_cast<floatx4*>(mine)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  __syncthreads();
-  const uint32_t row0 = routes[0].first;
-  if (n) {
-    const MoeRoute end = routes[(u1 - 1) / groups - a0];
-    for (uint32_t i = tid; i < end.first + end.count - row0; i += kDownWaves * 64) pairs[i] = p.pair[(size_t)b * kBlock * p.top_k + row0 + i];
-  }
   __syncthreads();
   const uint16_t* const h0 = p.h + (size_t)b * kBlock * p.top_k * I + 8 * kq;
   // rows r0 .. of every expert (a second pass only where an expert has more than 16 tokens of the block)
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (row + e < route.count) {
-          const MoePair pair = pairs[route.first - row0 + row + e];
+          const MoePair pair = pairs[route.first + row + e];
           Columns* const to = reinterpret_cast<Columns*>(mine + pair.token * N + C * l16);
           Columns y = *to;
 #pragma unroll
@@ -425,7 +447,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
       __builtin_amdgcn_sched_barrier(0);
     };
     if (wu0 >= wu1) break;
-    Unit t = settle(Unit{wu0, wu0 / groups - a0, wu0 % groups, true});
+    Unit t = settle(Unit{wu0, wu0 / groups, wu0 % groups, true});
     if (!t.there) continue;
     // Three units' weights and two units' rows ahead, the rows asked for before the weights of the same turn.
     Words ahead[kDownAhead];
@@ -511,10 +533,14 @@ hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream) {
   if (p.tokens == 1) hipLaunchKernelGGL(moe_scores_kernel<1>, dim3(p.experts), dim3(256), 0, stream, p);
   else hipLaunchKernelGGL(moe_scores_kernel<4>, dim3(p.experts, (p.tokens + 3) / 4), dim3(256), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
-  if (p.experts <= 64) hipLaunchKernelGGL(moe_routes_kernel<4>, dim3(blocks), dim3(1024), 0, stream, p);
-  else if (p.experts <= 128) hipLaunchKernelGGL(moe_routes_kernel<8>, dim3(blocks), dim3(1024), 0, stream, p);
-  else if (p.experts <= 256) hipLaunchKernelGGL(moe_routes_kernel<16>, dim3(blocks), dim3(1024), 0, stream, p);
-  else hipLaunchKernelGGL(moe_routes_kernel<32>, dim3(blocks), dim3(1024), 0, stream, p);
+  auto routes = [&](auto* one, auto* kern) {
+    if (p.tokens == 1) hipLaunchKernelGGL(one, dim3(1), dim3(64), 0, stream, p);
+    else hipLaunchKernelGGL(kern, dim3(blocks), dim3(1024), 0, stream, p);
+  };
+  if (p.experts <= 64) routes(&moe_route_kernel<4>, &moe_routes_kernel<4>);
+  else if (p.experts <= 128) routes(&moe_route_kernel<8>, &moe_routes_kernel<8>);
+  else if (p.experts <= 256) routes(&moe_route_kernel<16>, &moe_routes_kernel<16>);
+  else routes(&moe_route_kernel<32>, &moe_routes_kernel<32>);
   if (hipError_t e = hipGetLastError()) return e;
   // Waves of the up product: four have twice as many groups each to load ahead (46 -> 43 us of 2700 workgroups), eight are
   // done sooner where there are not enough workgroups for the compute units.
