@@ -29,9 +29,9 @@
 // Measured, in us, scores + routes + up + down; E experts of I inner and H hidden
 // columns, the active ones' weights over the last two: 1 token, E 64, top 8, I
 // 1024, H 2048: 3 + 3 + 8 + 8 (latency: one wait for memory each).  8 tokens, E 8,
-// top 2, I 8192, H 4096: 5 + 4 + 49 + 36 (374 MB, 4.4 TB/s).  33 tokens, E 128, top
-// 8, I 768, H 2048: 6 + 8 + 41 + 31 (274 MB, 3.8 TB/s).  64 tokens, E 60, top 4, I
-// 1408, H 2048: 6 + 6 + 40 + 31 (262 MB, 3.7 TB/s).  A copy reaches 5.2 TB/s.
+// top 2, I 8192, H 4096: 5 + 5 + 49 + 36 (374 MB, 4.4 TB/s).  33 tokens, E 128, top
+// 8, I 768, H 2048: 6 + 8 + 41 + 30 (274 MB, 3.9 TB/s).  64 tokens, E 60, top 4, I
+// 1408, H 2048: 6 + 6 + 40 + 30 (262 MB, 3.7 TB/s).  A copy reaches 5.2 TB/s.
 
 #include "attention_common.hpp"
 #include "common.hpp"
@@ -43,7 +43,6 @@ namespace {
 
 constexpr uint32_t kBlock = kMoeBlock;   // tokens of a block (bits of a mask)
 constexpr int kDownWaves = 8;
-constexpr int kDownAhead = 3;   // units' weights on the way to a wave of the down product
 
 typedef unsigned long long u64;
 
@@ -262,6 +261,24 @@ struct Rows {
   half8_t v[4];
 };
 
+// Adds the product of 16 rows with a group's words to acc.
+__device__ __forceinline__ void multiply(floatx4 (&acc)[C], const Words& v, const Rows& rows) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    // one column set's operands at a time: unpacked ahead they take more registers than there are
+    __builtin_amdgcn_sched_barrier(0);
+    floatx4 c = {};
+    half8_t w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) w[s] = v.operand(s, i);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[s], w[s], c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(c[e], v.scale(i), acc[i][e]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // N columns of act(x G) * (x U) for the tokens of one active expert, 16 of them at a time
 template <int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
@@ -294,27 +311,6 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) v.v[s] = *reinterpret_cast<const half8_t*>(x + (g < groups ? g : groups - 1) * kGroup + 32 * s);
     };
-    auto multiply = [&](const Group& v, const Rows& rows) {
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const Words& w = which ? v.up : v.gate;
-          // one column set's operands at a time: unpacked ahead they take more registers than there are
-          __builtin_amdgcn_sched_barrier(0);
-          floatx4 c = {};
-          half8_t o[4];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) o[s] = w.operand(s, i);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[s], o[s], c);
-          floatx4& sum = which ? up[i] : gate[i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(c[e], w.scale(i), sum[e]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
     // Loads come back in order: the next group's rows and then its weights are on the way while one is multiplied.
     Rows rows;
     read(rows, wave);
@@ -324,7 +320,8 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
       const Rows with = rows;
       read(rows, g + WAVES);
       load(ahead, g + WAVES);
-      multiply(now, with);
+      multiply(gate, now.gate, with);
+      multiply(up, now.up, with);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -351,6 +348,12 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
     __syncthreads();
   }
 }
+
+// Units (a group's weights and rows) on the way to a wave of the down product, one after the other into the same registers:
+// copied from register to register, a unit is waited for as soon as it is asked for (31.3 us instead of 30.0 for 33 tokens of
+// 128 experts).  In the up product, with two matrices' weights for each of x's rows, the copies cost less than the loads gain by
+// being sent before the product instead of after it (41 us, 49 in turns).
+constexpr int kAhead = 3;
 
 // N hidden columns of one part of the (active expert, group) units.  A wave takes consecutive ones and adds an expert's
 // result, times the shares, to sums of its own in LDS, [token][column]; the waves' sums are added at the end.
@@ -427,54 +430,34 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
         for (int i = 0; i < C; ++i) acc[i][e] = 0.f;
       }
     };
-    auto multiply = [&](const Words& v, const Rows& rows, uint32_t a) {
-      if (a != expert) {
-        flush();
-        expert = a;
-      }
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        __builtin_amdgcn_sched_barrier(0);   // (as above)
-        floatx4 c = {};
-        half8_t w[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) w[s] = v.operand(s, i);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[s], w[s], c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(c[e], v.scale(i), acc[i][e]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
     if (wu0 >= wu1) break;
     Unit t = settle(Unit{wu0, wu0 / groups, wu0 % groups, true});
     if (!t.there) continue;
-    // Three units' weights and two units' rows ahead, the rows asked for before the weights of the same turn.
-    Words ahead[kDownAhead];
-    Unit next = after(t), second = after(next), furthest = t;
-    Rows rows, rows_next;
-    read(rows, t);
-    read(rows_next, next);
-#pragma unroll
-    for (int j = 0; j < kDownAhead; ++j) {
-      load(ahead[j], furthest);
-      if (j + 1 < kDownAhead) furthest = after(furthest);
-    }
-#pragma unroll 1
-    for (;;) {
-      const Words now = ahead[0];
-      const Rows with = rows;
-#pragma unroll
-      for (int j = 0; j + 1 < kDownAhead; ++j) ahead[j] = ahead[j + 1];
-      rows = rows_next;
-      read(rows_next, second);
-      furthest = after(furthest);
-      load(ahead[kDownAhead - 1], furthest);
-      multiply(now, with, t.a);
-      if (!next.there) break;
+    Words words[kAhead];
+    Rows rows[kAhead];
+    Unit next = after(t), second = after(next);
+    read(rows[0], t);
+    load(words[0], t);
+    read(rows[1], next);
+    load(words[1], next);
+    read(rows[2], second);
+    load(words[2], second);
+    auto step = [&](int j) {
+      if (t.a != expert) {
+        flush();
+        expert = t.a;
+      }
+      multiply(acc, words[j], rows[j]);
+      const Unit third = after(second);
+      read(rows[j], third);
+      load(words[j], third);
+      const bool more = next.there;
       t = next;
       next = second;
-      second = after(second);
+      second = third;
+      return more;
+    };
+    while (step(0) && step(1) && step(2)) {
     }
     flush();
   }
