@@ -223,3 +223,36 @@ def test_refusals():
         kaio.kaio_linear_w8a8(x.half().repeat(10, 1), w, ws, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         kaio.kaio_linear_w8a8(x[:, :24].contiguous(), w[:, :24].contiguous(), ws, x_scale=xs)
+
+
+@pytest.mark.parametrize("m,n", [(1, 520), (8, 4096), (16, 8200), (17, 200), (61, 2043), (300, 1000), (2304, 4099)])
+def test_rows_behind_the_last_stay_as_they_were(m, n):
+    k = 272
+    x = torch.randn(m, k, device=DEV).half()
+    w = torch.randint(-127, 128, (n, k), device=DEV, dtype=torch.int8)
+    ws = torch.rand(n, device=DEV)
+    buf = torch.full((m * n + 4096,), 7.0, dtype=torch.float16, device=DEV)
+    need = kaio.lib().kaio_linear_w8a8_workspace_size(m, n, k, 0)
+    scratch = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    kaio.kaio_linear_w8a8(x, w, ws, y=buf[:m * n].view(m, n), workspace=scratch)
+    torch.cuda.synchronize()
+    assert (buf[m * n:] == 7).all() and (scratch[need:] == 77).all()
+    q, s = kaio.kaio_quantize_rows(x)
+    assert torch.equal(buf[:m * n].view(m, n), kaio.kaio_linear_w8a8(q, w, ws, x_scale=s))
+
+
+def test_calls_on_two_streams_at_once():
+    n, k = 2043, 1040
+    w, ws = torch.randint(-127, 128, (n, k), device=DEV, dtype=torch.int8), torch.rand(n, device=DEV)
+    xs = [torch.randn(m, k, device=DEV).bfloat16() for m in (1, 9, 40, 130, 700)]
+    want = [kaio.kaio_linear_w8a8(x, w, ws, activation="silu") for x in xs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] += [kaio.kaio_linear_w8a8(x, w, ws, activation="silu") for x in (xs if i else xs[::-1])]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, y in enumerate(got[i]):
+            assert torch.equal(y, (want if i else want[::-1])[j % 5])

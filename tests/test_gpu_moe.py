@@ -192,3 +192,34 @@ def test_refusals():
         for other in (t[:4], t.float() if t.dtype != torch.float16 else t.bfloat16(), t.cpu(), t.transpose(0, 1)):
             with pytest.raises((TypeError, ValueError)):
                 kaio.KaioExperts(*[other if j == i else a for j, a in enumerate(ws)])
+
+
+@pytest.mark.parametrize("t", [1, 5, 64, 67])
+def test_rows_behind_the_last_stay_as_they_were(t):
+    ws = weights(12, 256, 128)
+    experts, buf = kaio.KaioExperts(*[to_dev(a) for a in ws]), torch.full((t + 70, 256), 7.0, dtype=torch.float16, device=DEV)
+    x = to_dev(tokens(t, 256))
+    need = kaio.lib().kaio_moe_w4a16_workspace_size(experts._ref, t, 3)
+    scratch = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    kaio.kaio_moe_w4a16(x, experts, 3, y=buf[:t], workspace=scratch)
+    torch.cuda.synchronize()
+    assert (buf[t:] == 7).all() and (scratch[need:] == 77).all()
+    assert torch.equal(buf[:t], kaio.kaio_moe_w4a16(x, experts, 3))
+
+
+def test_calls_on_two_streams_at_once():
+    ws = weights(40, 512, 384)
+    experts = kaio.KaioExperts(*[to_dev(a) for a in ws])
+    xs = [to_dev(tokens(t, 512, t)) for t in (1, 3, 33, 64, 90)]
+    want = [kaio.kaio_moe_w4a16(x, experts, 4) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] += [kaio.kaio_moe_w4a16(x, experts, 4) for x in (xs if i else xs[::-1])]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, y in enumerate(got[i]):
+            assert torch.equal(y, (want if i else want[::-1])[j % 5])
