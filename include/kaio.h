@@ -375,7 +375,7 @@ typedef struct kaio_experts {
  *   E(t)    = the top_k experts of largest z[t, e] (ties: the lowest e)
  *   p[t, e] = exp(z[t, e]) / sum exp(z[t, .]), the sum over E(t) with
  *             normalize, else over all experts
- *   h[t, e] = act(x[t] . Wgate[e]) * (x[t] . Wup[e])            f16[inner]
+ *   h[t, e] = act(x[t] . Wgate[e]) * (x[t] . Wup[e])            [inner]
  *   y[t]    = sum over E(t) of p[t, e] * (h[t, e] . Wdown[e])  + r[t]
  *
  *   x  f16[tokens, hidden]     residual  the same shape, or NULL
@@ -385,10 +385,12 @@ typedef struct kaio_experts {
  *              must not overlap in time.
  *
  * z is summed in f64, so experts come in the order of the formula.  A score
- * that is NaN comes after every number.  Products are accumulated in f32, h is
- * rounded to f16 (half a step; past 65504 it is infinite, as any f16
- * activation), y is rounded once.  A token sees its own experts only, whatever
- * the others hold.  Results are the same on every run.
+ * that is NaN comes after every number.  Products are accumulated in f32.  h
+ * has f32's range and is kept to 2^-22 of itself and 2^-23 of the largest of
+ * its 32 columns (of inner, from a multiple of 32 on); y is rounded once.  A
+ * token sees its own experts only, whatever the others hold.  Results are the
+ * same on every run.  (Blocks of 64 tokens some of whose h are, 32 columns'
+ * largest, 4096 or more, or under 2^-16 but not zero, take longer.)
  *
  * Made for few tokens: the chosen experts' weights are read once for each 64
  * tokens.  More are computed as rightly, 64 at a time.

@@ -809,6 +809,8 @@ kaio_status kaio_moe_w4a16(const kaio_experts* e, const void* x, const void* res
   p.active = reinterpret_cast<uint32_t*>(at + plan.active);
   p.arrived = reinterpret_cast<uint32_t*>(at + plan.arrived);
   p.h = reinterpret_cast<uint16_t*>(at + plan.h);
+  p.bin = reinterpret_cast<uint8_t*>(at + plan.bin);
+  p.odd = reinterpret_cast<uint32_t*>(at + plan.odd);
   p.partial = reinterpret_cast<float*>(at + plan.partial);
   return launched(op, kaio::launch_moe_w4a16(p, static_cast<hipStream_t>(stream)));
 }

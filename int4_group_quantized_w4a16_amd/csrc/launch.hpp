@@ -302,12 +302,14 @@ struct Moe {
   MoeRoute* route;            // [blocks, slots]
   MoePair* pair;              // [tokens * top_k]
   uint32_t *active, *arrived; // [blocks], [blocks, hidden / kMoeStrip]
-  uint16_t* h;                // [tokens * top_k, inner]
+  uint16_t* h;                // [tokens * top_k, 2, inner]: high and low numbers
+  uint8_t* bin;               // [tokens * top_k, inner / kMoeStrip]: their exponents
+  uint32_t* odd;              // [blocks]: whether there are unusual ones
   float* partial;             // [splits, tokens, hidden] where splits > 1
 };
 struct MoePlan {
   uint64_t blocks, slots, splits;
-  uint64_t route, pair, active, arrived, h, partial, bytes;   // offsets in the workspace (scores come first)
+  uint64_t route, pair, active, arrived, h, bin, odd, partial, bytes;   // offsets in the workspace (scores come first)
 };
 constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, uint64_t inner, uint64_t top_k) {
   MoePlan a{};
@@ -329,7 +331,9 @@ constexpr MoePlan moe_plan(uint64_t tokens, uint64_t experts, uint64_t hidden, u
   a.pair = take(tokens * top_k * sizeof(MoePair));
   a.active = take(a.blocks * 4);
   a.arrived = take(a.blocks * (hidden / kMoeStrip) * 4);
-  a.h = take(tokens * top_k * inner * 2);
+  a.h = take(tokens * top_k * inner * 4);
+  a.bin = take(tokens * top_k * (inner / kMoeStrip));
+  a.odd = take(a.blocks * 4);
   a.partial = take(a.splits > 1 ? a.splits * tokens * hidden * 4 : 0);
   a.bytes = at;
   return a;

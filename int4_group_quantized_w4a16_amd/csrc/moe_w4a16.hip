@@ -20,18 +20,20 @@
 //   out the groups along the hidden axis, 16 of the expert's tokens at a time.
 //   One workgroup is launched for every expert that could be active (the host
 //   does not know how many are), the rest return.
+// * h between them: two f16 numbers each and an exponent per 32 columns (below).
 // * down: one workgroup per 32 hidden columns and a part of the (active expert,
 //   group) units, each of its waves a run of consecutive ones, so that an
-//   expert's result stays in registers until the next expert.  The waves' sums
+//   expert's result stays in registers until the next expert.  Eight rows of h
+//   at a time, sixteen of experts that have more than eight.  The waves' sums
 //   are in LDS, the parts' in the workspace, in f32, and the last workgroup to
 //   arrive adds them in order: no sum depends on who came first.
 //
 // Measured, in us, scores + routes + up + down; E experts of I inner and H hidden
 // columns, the active ones' weights over the last two: 1 token, E 64, top 8, I
 // 1024, H 2048: 3 + 3 + 8 + 8 (latency: one wait for memory each).  8 tokens, E 8,
-// top 2, I 8192, H 4096: 5 + 5 + 49 + 36 (374 MB, 4.4 TB/s).  33 tokens, E 128, top
-// 8, I 768, H 2048: 6 + 8 + 41 + 30 (274 MB, 3.9 TB/s).  64 tokens, E 60, top 4, I
-// 1408, H 2048: 6 + 6 + 40 + 30 (262 MB, 3.7 TB/s).  A copy reaches 5.2 TB/s.
+// top 2, I 8192, H 4096: 5 + 5 + 54 + 40 (374 MB, 4.0 TB/s).  33 tokens, E 128, top
+// 8, I 768, H 2048: 6 + 8 + 42 + 30 (274 MB, 3.8 TB/s).  64 tokens, E 60, top 4, I
+// 1408, H 2048: 5 + 6 + 41 + 34 (262 MB, 3.5 TB/s).  A copy reaches 5.2 TB/s.
 
 #include "attention_common.hpp"
 #include "common.hpp"
@@ -161,7 +163,10 @@ template <int V>
 __global__ void __launch_bounds__(64) moe_route_kernel(Moe p) {
   const uint32_t lane = threadIdx.x;
   for (uint32_t i = lane; i < p.hidden / kMoeStrip; i += 64) p.arrived[i] = 0;
-  if (lane == 0) p.active[0] = p.top_k;
+  if (lane == 0) {
+    p.active[0] = p.top_k;
+    p.odd[0] = 0;
+  }
   const Choice c = choose<V>(p, 0);
   if (lane < p.top_k) {
     p.route[lane] = MoeRoute{c.expert, lane, 1};
@@ -214,7 +219,10 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
     }
     active += a;
   }
-  if (tid == 0) p.active[b] = active;
+  if (tid == 0) {
+    p.active[b] = active;
+    p.odd[b] = 0;
+  }
   if (any) {
     p.route[(size_t)b * p.slots + place - 1] = MoeRoute{tid, rows - count, count};
     s.first[tid] = rows - count;
@@ -261,22 +269,63 @@ struct Rows {
   half8_t v[4];
 };
 
-// Adds the product of 16 rows with a group's words to acc.
-__device__ __forceinline__ void multiply(floatx4 (&acc)[C], const Words& v, const Rows& rows) {
+// Adds the products of TILES times 16 rows with a group's words to acc.
+template <int TILES>
+__device__ __forceinline__ void multiply(floatx4 (&acc)[TILES][C], const Words& v, const Rows (&rows)[TILES]) {
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     // one column set's operands at a time: unpacked ahead they take more registers than there are
     __builtin_amdgcn_sched_barrier(0);
-    floatx4 c = {};
     half8_t w[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) w[s] = v.operand(s, i);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows.v[s], w[s], c);
+    for (int t = 0; t < TILES; ++t) {
+      floatx4 c = {};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(c[e], v.scale(i), acc[i][e]);
+      for (int s = 0; s < 4; ++s) c = mfma16x16x32(rows[t].v[s], w[s], c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][i][e] = __builtin_fmaf(c[e], v.scale(i), acc[t][i][e]);
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// ---- h between the products ---------------------------------------------------
+// f16 alone would cost h 13 of its 24 bits, and all of it past 65504 or far below 2^-14.  It is two f16 numbers instead: with
+// t = h / 2^e, high = f16(t) and low = f16((t - high) 2^11), together within 2^-22 of h and 2^-36 of 2^e.  e is that of a
+// strip's N columns of a row, from the largest finite magnitude in them: where that is in [2^(28 b - 156), 2^(28 b - 128)), b the
+// strip's bin, 1 to 10, e is 28 b - 143, which brings it to [2^-13, 2^15).  The usual bin, 5, is 2^-16 to 2^12.  Bin 0: no finite
+// one but zeros (of any e).  Infinities and NaN are high themselves.
+//
+// The high and the low numbers are rows of their own to the matrix instruction, one after the other, so that eight rows of h
+// fill the 16 that it takes; the low row's sums count 2^-11.  Strips that add up must be of one e: where a block has any of an
+// odd bin (neither 0 nor the usual one) the down product takes the units once for each bin, without the strips of others
+// (33 tokens of 128 experts: 143 us in all instead of 86).
+constexpr uint32_t kUsualBin = 5;
+constexpr float kLow = 0x1p-11f;
+__device__ __forceinline__ int exponent_of(uint32_t bin) { return 28 * (int)(bin ? bin : kUsualBin) - 143; }
+__device__ __forceinline__ uint32_t bin_of(uint32_t most) { return most ? ((most >> 23) + 29) / 28 : 0; }   // f32's bits
+static_assert(29 / 28 == 1 && (254 + 29) / 28 == 10 && (127 - 16 + 29) / 28 == kUsualBin && (127 + 11 + 29) / 28 == kUsualBin, "bins");
+struct Pieces {
+  uint16_t high, low;
+  uint32_t bin;
+};
+// of one number of a strip per lane, 32 lanes to a strip
+__device__ __forceinline__ Pieces pieces(float h) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, h) & 0x7FFFFFFFu;
+  const bool finite = bits < 0x7F800000u;
+  uint32_t most = finite ? bits : 0;
+#pragma unroll
+  for (int x = 16; x; x >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)most, x);
+    most = most > o ? most : o;
+  }
+  const uint32_t bin = bin_of(most);
+  const float t = __builtin_ldexpf(h, -exponent_of(bin));
+  const _Float16 high = (_Float16)t;
+  const _Float16 low = finite ? (_Float16)((t - (float)high) * (1 / kLow)) : (_Float16)0.f;
+  return Pieces{__builtin_bit_cast(uint16_t, high), __builtin_bit_cast(uint16_t, low), bin};
 }
 
 // N columns of act(x G) * (x U) for the tokens of one active expert, 16 of them at a time
@@ -306,19 +355,19 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
     load(ahead, wave);   // (the first ones before their rows are known)
     const uint32_t row = r0 + l16 < route.count ? r0 + l16 : route.count - 1;   // past the last that one
     const uint16_t* const x = p.x + ((size_t)b * kBlock + pairs[row].token) * H + 8 * kq;
-    floatx4 gate[C] = {}, up[C] = {};
+    floatx4 gate[1][C] = {}, up[1][C] = {};
     auto read = [&](Rows& v, uint32_t g) {   // past the last group that one
 #pragma unroll
       for (int s = 0; s < 4; ++s) v.v[s] = *reinterpret_cast<const half8_t*>(x + (g < groups ? g : groups - 1) * kGroup + 32 * s);
     };
     // Loads come back in order: the next group's rows and then its weights are on the way while one is multiplied.
-    Rows rows;
-    read(rows, wave);
+    Rows rows[1];
+    read(rows[0], wave);
 #pragma unroll 1
     for (uint32_t g = wave; g < groups; g += WAVES) {
       const Group now = ahead;
-      const Rows with = rows;
-      read(rows, g + WAVES);
+      const Rows with[1] = {rows[0]};
+      read(rows[0], g + WAVES);
       load(ahead, g + WAVES);
       multiply(gate, now.gate, with);
       multiply(up, now.up, with);
@@ -327,7 +376,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
     for (int e = 0; e < 4; ++e) {
       Columns vg, vu;
 #pragma unroll
-      for (int i = 0; i < C; ++i) vg[i] = gate[i][e], vu[i] = up[i][e];
+      for (int i = 0; i < C; ++i) vg[i] = gate[0][i][e], vu[i] = up[0][i][e];
       *reinterpret_cast<Columns*>(&part[wave][0][4 * kq + e][C * l16]) = vg;
       *reinterpret_cast<Columns*>(&part[wave][1][4 * kq + e][C * l16]) = vu;
     }
@@ -342,8 +391,14 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
         z += part[w][1][o / N][c];
       }
       activations<1>(y, p.act);
-      // rounded to f16, as the next product's other operand
-      p.h[((size_t)b * kBlock * p.top_k + route.first + at) * I + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)(y[0] * z));
+      const Pieces h = pieces(y[0] * z);
+      const size_t row = (size_t)b * kBlock * p.top_k + route.first + at;
+      p.h[2 * row * I + n0 + c] = h.high;
+      p.h[(2 * row + 1) * I + n0 + c] = h.low;
+      if (c == 0) {
+        p.bin[(row * I + n0) / N] = (uint8_t)h.bin;
+        if (h.bin && h.bin != kUsualBin) __hip_atomic_store(&p.odd[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
     __syncthreads();
   }
@@ -355,111 +410,179 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
 // being sent before the product instead of after it (41 us, 49 in turns).
 constexpr int kAhead = 3;
 
+struct DownShared {
+  MoeRoute routes[kMoeMaxExperts];      // of the block's active experts
+  MoePair pairs[kBlock * kMoeMaxTop];   // and their rows
+  uint32_t bins;                        // that the block has, as bits
+  uint32_t last;
+};
+
+// A wave's units [first, last), TILES times 8 rows from r0 on, of those experts of the block that have LEAST to MOST rows from
+// there on.  Adds an expert's result, times the shares, to mine ([token][column]).  PICK: takes only the strips of `bin`.
+template <int TILES, int AHEAD, uint32_t LEAST, uint32_t MOST, bool PICK>
+__device__ __forceinline__ void down_rows(const Moe& p, const DownShared& shared, float* mine, uint32_t r0, uint32_t first,
+                                          uint32_t last, uint32_t b, uint32_t n0, uint32_t bin) {
+  const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, kq = lane >> 4, col = n0 + C * l16;
+  const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup;
+  const MoeRoute* const routes = shared.routes;
+  const size_t row0 = (size_t)b * kBlock * p.top_k;
+  const uint16_t* const h0 = p.h + 2 * row0 * I + (size_t)(l16 & 1) * I + 8 * kq;
+  // past the last unit that one, and not there
+  struct Unit {
+    uint32_t u, a, g;   // the unit, its expert's place in routes, its group
+    bool there;
+  };
+  auto settle = [&](Unit t) {
+    auto takes = [&](uint32_t count) { return count >= r0 + LEAST && count <= r0 + MOST; };
+    while (t.there && !takes(routes[t.a].count)) {   // on to the next expert
+      t.u += groups - t.g;
+      ++t.a;
+      t.g = 0;
+      t.there = t.u < last;
+    }
+    return t;
+  };
+  auto after = [&](const Unit& t) {
+    if (t.u + 1 >= last) return Unit{t.u, t.a, t.g, false};
+    const bool same = t.g + 1 < groups;
+    const Unit n = settle(Unit{t.u + 1, same ? t.a : t.a + 1, same ? t.g + 1 : 0, true});
+    return n.there ? n : Unit{t.u, t.a, t.g, false};
+  };
+  auto load = [&](Words& v, const Unit& t) {
+    const size_t e = __builtin_amdgcn_readfirstlane(routes[t.a].expert);
+    v.load(p.w_down + e * (I / 8) * H, p.s_down + e * groups * H, H, t.g, kq, col, t.there);
+  };
+  // a lane's row of tile i, of the block's; past the last row that one, whose results go nowhere
+  auto row_of = [&](const Unit& t, int i) {
+    const uint32_t row = r0 + 8 * i + l16 / 2, count = routes[t.a].count;
+    return routes[t.a].first + (row < count ? row : count - 1);
+  };
+  auto read = [&](Rows (&v)[TILES], const Unit& t) {
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const uint16_t* const h = h0 + (size_t)row_of(t, i) * 2 * I + t.g * kGroup;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[i].v[s] = *reinterpret_cast<const half8_t*>(h + 32 * s);
+    }
+  };
+  auto pick = [&](Rows (&v)[TILES], const Unit& t) {
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+      const uint32_t bins = *reinterpret_cast<const uint32_t*>(p.bin + (row0 + row_of(t, i)) * (I / N) + t.g * (kGroup / N));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if ((bins >> 8 * s & 0xFF) != bin) v[i].v[s] = half8_t{};
+      }
+    }
+  };
+  static_assert(kGroup / N == 4, "the strips of a group are the steps of its product, and their bins a word");
+  floatx4 acc[TILES][C] = {};
+  uint32_t expert = ~0u;   // whose rows acc holds
+  auto flush = [&] {
+    if (expert == ~0u) return;
+    const MoeRoute route = routes[expert];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {   // of a lane's four sums two rows', high and low
+        const uint32_t row = r0 + 8 * i + 2 * kq + e / 2;
+        if (row < route.count) {
+          const MoePair pair = shared.pairs[route.first + row];
+          Columns* const to = reinterpret_cast<Columns*>(mine + pair.token * N + C * l16);
+          Columns y = *to;
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            y[c] = __builtin_fmaf(__builtin_ldexpf(__builtin_fmaf(acc[i][c][e + 1], kLow, acc[i][c][e]), exponent_of(bin)), pair.share, y[c]);
+          *to = y;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[i][c][e] = acc[i][c][e + 1] = 0.f;
+      }
+  };
+  Unit next[AHEAD];   // the unit to multiply and those on the way
+  next[0] = settle(Unit{first, first / groups, first % groups, true});
+  if (!next[0].there) return;
+  Words words[AHEAD];
+  Rows rows[AHEAD][TILES];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    if (i) next[i] = after(next[i - 1]);
+    read(rows[i], next[i]);
+    load(words[i], next[i]);
+  }
+  auto step = [&](int j) {
+    if (next[0].a != expert) {
+      flush();
+      expert = next[0].a;
+    }
+    if (PICK) pick(rows[j], next[0]);
+    multiply(acc, words[j], rows[j]);
+    const Unit n = after(next[AHEAD - 1]);
+    read(rows[j], n);
+    load(words[j], n);
+#pragma unroll
+    for (int i = 0; i + 1 < AHEAD; ++i) next[i] = next[i + 1];
+    next[AHEAD - 1] = n;
+    return next[0].there;
+  };
+  if constexpr (AHEAD == 3) {
+    while (step(0) && step(1) && step(2)) {
+    }
+  } else {
+    static_assert(AHEAD == 1);
+    while (step(0)) {
+    }
+  }
+  flush();
+}
+
 // N hidden columns of one part of the (active expert, group) units.  A wave takes consecutive ones and adds an expert's
 // result, times the shares, to sums of its own in LDS, [token][column]; the waves' sums are added at the end.
 __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
   extern __shared__ __attribute__((aligned(16))) float sums[];   // [wave][tokens of the block][N]
-  __shared__ MoeRoute routes[kMoeMaxExperts];            // of the block's active experts
-  __shared__ MoePair pairs[kBlock * kMoeMaxTop];         // and their rows
-  __shared__ uint32_t last;
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
-  const uint32_t H = p.hidden, I = p.inner, groups = I / kGroup, strips = H / N;
-  const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * N, col = n0 + C * l16;
+  __shared__ DownShared shared;
+  constexpr uint32_t kThreads = kDownWaves * 64;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t H = p.hidden, groups = p.inner / kGroup, strips = H / N;
+  const uint32_t b = blockIdx.y, strip = blockIdx.x % strips, split = blockIdx.x / strips, n0 = strip * N;
   const uint32_t tokens = p.tokens - b * kBlock < kBlock ? p.tokens - b * kBlock : kBlock;
   // All of them at once, whichever this part needs, and before the number of active ones is known (past it the workspace holds
   // anything): one wait for memory instead of three.
-  const uint32_t active = p.active[b];   // (first: after stores the compiler would load it by vectors)
-  for (uint32_t i = tid; i < p.slots; i += kDownWaves * 64) routes[i] = p.route[(size_t)b * p.slots + i];
-  for (uint32_t i = tid; i < tokens * p.top_k; i += kDownWaves * 64) pairs[i] = p.pair[(size_t)b * kBlock * p.top_k + i];
+  const uint32_t active = p.active[b], odd = p.odd[b];   // (first: after stores the compiler would load them by vectors)
+  for (uint32_t i = tid; i < p.slots; i += kThreads) shared.routes[i] = p.route[(size_t)b * p.slots + i];
+  const size_t row0 = (size_t)b * kBlock * p.top_k;
+  for (uint32_t i = tid; i < tokens * p.top_k; i += kThreads) shared.pairs[i] = p.pair[row0 + i];
+  if (tid == 0) shared.bins = 0;
   const u64 units = (u64)active * groups;
   const uint32_t u0 = (uint32_t)(units * split / p.splits), u1 = (uint32_t)(units * (split + 1) / p.splits), n = u1 - u0;
   const uint32_t wu0 = u0 + n * wave / kDownWaves, wu1 = u0 + n * (wave + 1) / kDownWaves;
   float* const mine = sums + wave * tokens * N;
   for (uint32_t i = lane; i < tokens * N / 4; i += 64) reinterpret_cast<floatx4*>(mine)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
-  const uint16_t* const h0 = p.h + (size_t)b * kBlock * p.top_k * I + 8 * kq;
-  // rows r0 .. of every expert (a second pass only where an expert has more than 16 tokens of the block)
-  for (uint32_t r0 = 0; r0 < tokens; r0 += 16) {
-    // the wave's units whose expert has such rows, one after the other; past the last that one, and not there
-    struct Unit {
-      uint32_t u, a, g;   // the unit, its expert's place in routes, its group
-      bool there;
-    };
-    auto settle = [&](Unit t) {
-      while (t.there && r0 >= routes[t.a].count) {   // on to the next expert
-        t.u += groups - t.g;
-        ++t.a;
-        t.g = 0;
-        t.there = t.u < wu1;
-      }
-      return t;
-    };
-    auto after = [&](const Unit& t) {
-      if (t.u + 1 >= wu1) return Unit{t.u, t.a, t.g, false};
-      const bool same = t.g + 1 < groups;
-      const Unit n = settle(Unit{t.u + 1, same ? t.a : t.a + 1, same ? t.g + 1 : 0, true});
-      return n.there ? n : Unit{t.u, t.a, t.g, false};
-    };
-    auto load = [&](Words& v, const Unit& t) {
-      const size_t e = __builtin_amdgcn_readfirstlane(routes[t.a].expert);
-      v.load(p.w_down + e * (I / 8) * H, p.s_down + e * groups * H, H, t.g, kq, col, t.there);
-    };
-    auto read = [&](Rows& v, const Unit& t) {   // past the last row that one, whose results go nowhere
-      const uint32_t first = routes[t.a].first, count = routes[t.a].count, row = r0 + l16;
-      const uint16_t* const h = h0 + (size_t)(first + (row < count ? row : count - 1)) * I + t.g * kGroup;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) v.v[s] = *reinterpret_cast<const half8_t*>(h + 32 * s);
-    };
-    floatx4 acc[C] = {};
-    uint32_t expert = ~0u;   // whose rows acc holds
-    auto flush = [&] {
-      if (expert == ~0u) return;
-      const MoeRoute route = routes[expert];
-      const uint32_t row = r0 + 4 * kq;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (row + e < route.count) {
-          const MoePair pair = pairs[route.first + row + e];
-          Columns* const to = reinterpret_cast<Columns*>(mine + pair.token * N + C * l16);
-          Columns y = *to;
-#pragma unroll
-          for (int i = 0; i < C; ++i) y[i] = __builtin_fmaf(acc[i][e], pair.share, y[i]);
-          *to = y;
-        }
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i][e] = 0.f;
-      }
-    };
-    if (wu0 >= wu1) break;
-    Unit t = settle(Unit{wu0, wu0 / groups, wu0 % groups, true});
-    if (!t.there) continue;
-    Words words[kAhead];
-    Rows rows[kAhead];
-    Unit next = after(t), second = after(next);
-    read(rows[0], t);
-    load(words[0], t);
-    read(rows[1], next);
-    load(words[1], next);
-    read(rows[2], second);
-    load(words[2], second);
-    auto step = [&](int j) {
-      if (t.a != expert) {
-        flush();
-        expert = t.a;
-      }
-      multiply(acc, words[j], rows[j]);
-      const Unit third = after(second);
-      read(rows[j], third);
-      load(words[j], third);
-      const bool more = next.there;
-      t = next;
-      next = second;
-      second = third;
-      return more;
-    };
-    while (step(0) && step(1) && step(2)) {
+  if (odd) {
+    // the bins of a group's strips are a word
+    const uint32_t* const bins = reinterpret_cast<const uint32_t*>(p.bin) + row0 * groups;
+    uint32_t seen = 0;
+    for (uint32_t i = tid; i < tokens * p.top_k * groups; i += kThreads) {
+      const uint32_t word = bins[i];
+      seen |= 1u << (word & 0xFF) | 1u << (word >> 8 & 0xFF) | 1u << (word >> 16 & 0xFF) | 1u << (word >> 24);
     }
-    flush();
+    if (seen) atomicOr(&shared.bins, seen);
+    __syncthreads();
+  }
+  // of the wave's experts the one with the most rows (of those that a lane looks at)
+  uint32_t most = 0;
+  if (wu0 < wu1)
+    for (uint32_t a = wu0 / groups + lane; a <= (wu1 - 1) / groups; a += 64) most = shared.routes[a].count > most ? shared.routes[a].count : most;
+  // (a second pass only where an expert has more than 16 tokens of the block)
+  for (uint32_t r0 = 0; __any(most > r0); r0 += 16) {
+    if (odd) {
+      for (uint32_t bins = shared.bins; bins; bins &= bins - 1)
+        down_rows<2, 1, 1, kBlock, true>(p, shared, mine, r0, wu0, wu1, b, n0, __builtin_ctz(bins));
+    } else {
+      down_rows<1, kAhead, 1, 8, false>(p, shared, mine, r0, wu0, wu1, b, n0, kUsualBin);
+      if (__any(most > r0 + 8)) down_rows<2, 1, 9, kBlock, false>(p, shared, mine, r0, wu0, wu1, b, n0, kUsualBin);
+    }
   }
   __syncthreads();
   // four columns of a token at a time
@@ -491,9 +614,9 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) moe_down_kernel(Moe p) {
   // the last of the strip's workgroups adds the parts, in order
   wait_vm<0>();
   __syncthreads();
-  if (tid == 0) last = __hip_atomic_fetch_add(&p.arrived[(size_t)b * strips + strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+  if (tid == 0) shared.last = __hip_atomic_fetch_add(&p.arrived[(size_t)b * strips + strip], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
   __syncthreads();
-  if (!last) return;
+  if (!shared.last) return;
   for (uint32_t o = tid; o < tokens * (N / 4); o += kDownWaves * 64) {
     const uint32_t off = o / (N / 4) * H + o % (N / 4) * 4;
     floatx4 y = {};

@@ -23,8 +23,8 @@ def choose(x, router, top_k, normalize):
 
 def moe(x, router, w_gate, s_gate, w_up, s_up, w_down, s_down, top_k, normalize=True, act="silu", residual=None):
     """(y, tolerance).  The tolerance: gate, up and down products 1e-5 of their sums of magnitudes (f32 accumulation) each,
-    the first through the activation's slope; h 2^-19 for the activation, 2^-22 for its product, half a step of f16 (2^-11,
-    below its normal numbers 2^-25); shares 2^-18 (arguments of exp up to 32 in f32, the hardware's exp, sum and quotient);
+    the first through the activation's slope; h 2^-19 for the activation, 2^-22 for its product, 2^-22 of itself and 2^-23
+    of the row's largest for what is kept of it (csrc/moe_w4a16.hip); shares 2^-18 (arguments of exp up to 32 in f32, the hardware's exp, sum and quotient);
     f32 sums over experts and parts (1e-5); half a step of f16 for y."""
     t, hidden = x.shape
     chosen, shares = choose(x, router, top_k, normalize)
@@ -39,7 +39,7 @@ def moe(x, router, w_gate, s_gate, w_up, s_up, w_down, s_down, top_k, normalize=
         a = ACT[act](gate)
         h = a * up
         dh = (SLOPE * 1e-5 * (np.abs(xr) @ np.abs(g)) * np.abs(up) + np.abs(a) * 1e-5 * (np.abs(xr) @ np.abs(u)) +
-              (2.0 ** -19 + 2.0 ** -22 + 2.0 ** -11) * np.abs(h) + 2.0 ** -25)
+              (2.0 ** -19 + 2.0 ** -21) * np.abs(h) + 2.0 ** -23 * np.abs(h).max(-1, keepdims=True))
         out = h @ d
         size = np.abs(h) @ np.abs(d)
         y[rows] += p * out
