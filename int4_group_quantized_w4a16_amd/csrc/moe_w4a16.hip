@@ -146,7 +146,13 @@ __device__ __forceinline__ Choice choose(const Moe& p, uint32_t token) {
     for (int v = 0; v < V; ++v) key[v] = e == lane * V + v ? 0 : key[v];
   }
   const double top = score_of(first);
-  auto part = [&](u64 k) { return __expf((float)(score_of(k) - top)); };
+  // to about a step of f32: what rounding the argument took comes back as a factor (the hardware's exponential of it alone is
+  // off by up to 2^-18, an argument's absolute error being its result's relative one)
+  auto part = [&](u64 k) {
+    const double d = score_of(k) - top;
+    const float f = (float)d, e = expf(f), rest = f > -110.f ? (float)(d - (double)f) : 0.f;   // (not of infinities: e is 0)
+    return __builtin_fmaf(e, rest, e);
+  };
   const float own = lane < p.top_k ? part(mine) : 0.f;
   float sum = own;
   if (!p.normalize) {   // those that were not chosen

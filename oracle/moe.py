@@ -24,7 +24,8 @@ def choose(x, router, top_k, normalize):
 def moe(x, router, w_gate, s_gate, w_up, s_up, w_down, s_down, top_k, normalize=True, act="silu", residual=None):
     """(y, tolerance).  The tolerance: gate, up and down products 1e-5 of their sums of magnitudes (f32 accumulation) each,
     the first through the activation's slope; h 2^-19 for the activation, 2^-22 for its product, 2^-22 of itself and 2^-23
-    of the row's largest for what is kept of it (csrc/moe_w4a16.hip); shares 2^-18 (arguments of exp up to 32 in f32, the hardware's exp, sum and quotient);
+    of the row's largest for what is kept of it (csrc/moe_w4a16.hip); shares 2^-18 (a step of f32 for exp,
+    the f32 sum of up to 512 of them, the quotient);
     f32 sums over experts and parts (1e-5); half a step of f16 for y."""
     t, hidden = x.shape
     chosen, shares = choose(x, router, top_k, normalize)
