@@ -256,9 +256,13 @@ int code_of(const E& e) {
   return code;
 }
 
-// Whether sizes that the operation defines and offers fit its launches.
+// Whether sizes that an operation defines fit its launches.
+bool linear8_fits(uint32_t m, uint32_t n, uint32_t k, bool rounds, uint64_t* x_bytes, uint64_t* w_bytes, uint64_t* out_bytes) {
+  return bytes_of(m, k, rounds ? 2 : 1, x_bytes) && bytes_of(n, k, 1, w_bytes) && bytes_of(m, n, 2, out_bytes) &&
+         kaio::linear8_wgs(m, n) <= kaio::kMaxWorkgroups && m <= kaio::kMaxWorkgroups && n < kaio::kMaxN;
+}
 bool moe_fits(const kaio_experts* e, uint32_t tokens, uint32_t top_k) {
-  if (tokens == 0 || tokens > kaio::kMoeMaxTokens || top_k == 0 || top_k > e->experts || top_k > kaio::kMoeMaxTop ||
+  if (e->group_size != 128 || tokens == 0 || tokens > kaio::kMoeMaxTokens || top_k == 0 || top_k > e->experts || top_k > kaio::kMoeMaxTop ||
       e->experts > kaio::kMoeMaxExperts || e->hidden == 0 || e->inner == 0 || e->hidden % 128 != 0 || e->inner % 128 != 0 ||
       e->hidden >= kaio::kMaxK || e->inner >= kaio::kMaxK)
     return false;
@@ -670,7 +674,10 @@ kaio_status kaio_quantize_rows(kaio_dtype dtype, const void* x, int8_t* q, float
 }
 
 size_t kaio_linear_w8a8_workspace_size(uint32_t m, uint32_t n, uint32_t k, int32_t int8_x) {
-  if (k % 16 != 0 || k > kaio::kLinear8MaxK || m == 0 || n == 0 || int8_x || kaio::linear8_rounds(m, n, k)) return 0;
+  uint64_t x_bytes = 0, w_bytes = 0, out_bytes = 0;
+  if (k % 16 != 0 || k > kaio::kLinear8MaxK || m == 0 || n == 0 || !linear8_fits(m, n, k, !int8_x, &x_bytes, &w_bytes, &out_bytes))
+    return 0;
+  if (int8_x || kaio::linear8_rounds(m, n, k)) return 0;
   return kaio::linear8_workspace(m, k);
 }
 
@@ -688,8 +695,7 @@ kaio_status kaio_linear_w8a8(kaio_dtype dtype, const void* x, const float* x_sca
   if (m == 0 || n == 0) return ok();
   const bool rounds = !x_scale;   // x is 16-bit and rounded here
   uint64_t x_bytes = 0, w_bytes = 0, out_bytes = 0;
-  if (!bytes_of(m, k, rounds ? 2 : 1, &x_bytes) || !bytes_of(n, k, 1, &w_bytes) || !bytes_of(m, n, 2, &out_bytes) ||
-      kaio::linear8_wgs(m, n) > kaio::kMaxWorkgroups || m > kaio::kMaxWorkgroups || n >= kaio::kMaxN)
+  if (!linear8_fits(m, n, k, rounds, &x_bytes, &w_bytes, &out_bytes))
     return fail(KAIO_ERR_INVALID_PROBLEM, op, "problem too large for one launch (m=%u, n=%u, k=%u)", m, n, k);
   const uint64_t need = kaio_linear_w8a8_workspace_size(m, n, k, !rounds);
   const struct { const void* p; const char* name; bool needed, used; } all[8] = {
