@@ -166,6 +166,16 @@ def _check(status: int):
         raise KaioError(status, kaio_last_error())
 
 
+def _call(device, fn, *args):
+    """fn(*args) of the C library, which launches on the current device, on ``device``."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args))
+
+
 def _stream(device, stream):
     import torch
     if stream is None:
@@ -238,8 +248,8 @@ def _qkv(fn, bits, x, w_q, w_k, w_v, s_q, s_k, s_v, q, k, v, stream):
     for dim in (M, N, K):
         if dim >= 2 ** 32:
             raise ValueError("dimension exceeds u32")
-    _check(fn(x.data_ptr(), *[t.data_ptr() for t in ws], *[t.data_ptr() for t in ss],
-              *[t.data_ptr() for t in outs], M, N, K, GROUP_SIZE, _stream(dev, stream)))
+    _call(dev, fn, x.data_ptr(), *[t.data_ptr() for t in ws], *[t.data_ptr() for t in ss], *[t.data_ptr() for t in outs], M,
+          N, K, GROUP_SIZE, _stream(dev, stream))
     return tuple(outs)
 
 
@@ -274,7 +284,7 @@ def kaio_gemm_f16f32(a, b, c=None, stream=None):
     _tensor(c, "c", (torch.float32,), a.device)
     if tuple(c.shape) != (M, N):
         raise ValueError(f"c must be [{M}, {N}]")
-    _check(lib().kaio_gemm_f16f32(a.data_ptr(), b.data_ptr(), c.data_ptr(), M, N, K, _stream(a.device, stream)))
+    _call(a.device, lib().kaio_gemm_f16f32, a.data_ptr(), b.data_ptr(), c.data_ptr(), M, N, K, _stream(a.device, stream))
     return c
 
 
@@ -304,9 +314,8 @@ def kaio_gemm_f16f32_bwd(a, b, grad, grad_a=None, grad_b=None, workspace=None, s
     if workspace is None:
         workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=a.device)
     _tensor(workspace, "workspace", (torch.uint8,), a.device, rank=1)
-    _check(lib().kaio_gemm_f16f32_bwd(a.data_ptr(), b.data_ptr(), grad.data_ptr(), grad_a.data_ptr(),
-                                      grad_b.data_ptr(), M, N, K, workspace.data_ptr(), workspace.numel(),
-                                      _stream(a.device, stream)))
+    _call(a.device, lib().kaio_gemm_f16f32_bwd, a.data_ptr(), b.data_ptr(), grad.data_ptr(), grad_a.data_ptr(),
+          grad_b.data_ptr(), M, N, K, workspace.data_ptr(), workspace.numel(), _stream(a.device, stream))
     return grad_a, grad_b
 
 
@@ -328,8 +337,8 @@ def kaio_dequant_group_bwd(dy, scale, group_size, dq=None, stream=None):
         raise ValueError("d_input shape != [outer, axis_size]")
     if outer >= 2 ** 31 or axis >= 2 ** 31:
         raise ValueError("sizes exceed i32")
-    _check(lib().kaio_dequant_group_bwd(codes[dy.dtype], outer, axis, group_size, dy.data_ptr(),
-                                        scale.data_ptr(), dq.data_ptr(), None, 0, _stream(dy.device, stream)))
+    _call(dy.device, lib().kaio_dequant_group_bwd, codes[dy.dtype], outer, axis, group_size, dy.data_ptr(),
+          scale.data_ptr(), dq.data_ptr(), None, 0, _stream(dy.device, stream))
     return dq
 
 
@@ -374,10 +383,9 @@ def kaio_linear_w4a16(x, w, s, bias=None, activation="none", residual=None, y=No
     for dim in (M, N, K):
         if dim >= 2 ** 32:
             raise ValueError("dimension exceeds u32")
-    _check(lib().kaio_linear_w4a16(x.data_ptr(), w.data_ptr(), s.data_ptr(),
-                                   None if bias is None else bias.data_ptr(),
-                                   None if residual is None else residual.data_ptr(), y.data_ptr(),
-                                   M, N, K, GROUP_SIZE, ACTIVATION_CODES[activation], _stream(dev, stream)))
+    _call(dev, lib().kaio_linear_w4a16, x.data_ptr(), w.data_ptr(), s.data_ptr(), None if bias is None else bias.data_ptr(),
+          None if residual is None else residual.data_ptr(), y.data_ptr(), M, N, K, GROUP_SIZE,
+          ACTIVATION_CODES[activation], _stream(dev, stream))
     return y
 
 
@@ -425,8 +433,8 @@ def kaio_quantize_rows(x, q=None, scale=None, stream=None):
     _like(scale, "scale", (torch.float32,), dev, (M,))
     if max(M, K) >= 2 ** 32:
         raise ValueError("dimension exceeds u32")
-    _check(lib().kaio_quantize_rows(2 if x.dtype == torch.float16 else 1, x.data_ptr(), q.data_ptr(), scale.data_ptr(), M, K,
-                                    _stream(dev, stream)))
+    _call(dev, lib().kaio_quantize_rows, 2 if x.dtype == torch.float16 else 1, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+          M, K, _stream(dev, stream))
     return q, scale
 
 
@@ -479,10 +487,9 @@ def kaio_linear_w8a8(x, w, w_scale, x_scale=None, bias=None, activation="none", 
         raise ValueError("dimension exceeds u32")
     need = lib().kaio_linear_w8a8_workspace_size(M, N, K, int(x_scale is not None))
     workspace = _scratch(need, workspace, dev, stream)
-    _check(lib().kaio_linear_w8a8(2 if dtype == torch.float16 else 1, x.data_ptr(), _ptr(x_scale), w.data_ptr(),
-                                  w_scale.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), M, N, K,
-                                  ACTIVATION_CODES[activation], _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                  _stream(dev, stream)))
+    _call(dev, lib().kaio_linear_w8a8, 2 if dtype == torch.float16 else 1, x.data_ptr(), _ptr(x_scale), w.data_ptr(),
+          w_scale.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), M, N, K, ACTIVATION_CODES[activation],
+          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev, stream))
     return y
 
 
@@ -558,9 +565,9 @@ def kaio_moe_w4a16(x, experts, top_k, normalize=True, activation="silu", residua
         raise ValueError("dimension exceeds u32")
     need = lib().kaio_moe_w4a16_workspace_size(experts._ref, T, top_k)
     workspace = _scratch(need, workspace, dev, stream)
-    _check(lib().kaio_moe_w4a16(experts._ref, x.data_ptr(), _ptr(residual), y.data_ptr(), T, top_k, int(bool(normalize)),
-                                ACTIVATION_CODES[activation], _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                _stream(dev, stream)))
+    _call(dev, lib().kaio_moe_w4a16, experts._ref, x.data_ptr(), _ptr(residual), y.data_ptr(), T, top_k,
+          int(bool(normalize)), ACTIVATION_CODES[activation], _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _stream(dev, stream))
     return y
 
 
@@ -658,9 +665,9 @@ def kaio_rope_append(q, k, v, positions, inv_freq, sections, paged, interleaved=
         raise ValueError(f"q_out must be {list(q.shape)}, got {list(q_out.shape)}")
     if T >= 2 ** 31 or q.shape[1] >= 2 ** 31:
         raise ValueError("dimension exceeds i32")
-    _check(lib().kaio_rope_append(p._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
-                                  inv_freq.data_ptr(), (ctypes.c_uint32 * axes)(*sections), axes, int(bool(interleaved)),
-                                  q_out.data_ptr(), T, q.shape[1], _stream(p.device, stream)))
+    _call(p.device, lib().kaio_rope_append, p._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
+          inv_freq.data_ptr(), (ctypes.c_uint32 * axes)(*sections), axes, int(bool(interleaved)), q_out.data_ptr(), T,
+          q.shape[1], _stream(p.device, stream))
     return q_out
 
 
@@ -695,7 +702,7 @@ def kaio_paged_attention(q, paged, max_new, scale, window=0, sinks=0, out=None, 
         workspace = _allocate(p.device, stream, lambda: torch.empty((need,), dtype=torch.uint8, device=p.device))
     if workspace is not None:
         _tensor(workspace, "workspace", (torch.uint8,), p.device, rank=1, any_offset=True)
-    _check(lib().kaio_paged_attention(p._ref, q.data_ptr(), out.data_ptr(), T, hq, max_new, scale, window, sinks,
-                                      None if workspace is None else workspace.data_ptr(),
-                                      0 if workspace is None else workspace.numel(), _stream(p.device, stream)))
+    _call(p.device, lib().kaio_paged_attention, p._ref, q.data_ptr(), out.data_ptr(), T, hq, max_new, scale, window, sinks,
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+          _stream(p.device, stream))
     return out
