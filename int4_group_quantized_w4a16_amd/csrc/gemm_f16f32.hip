@@ -681,9 +681,8 @@ hipError_t launch_dma(const uint16_t* a, uint32_t lda, const uint16_t* b, uint32
   const uint32_t mtiles = (mo + BM - 1) / BM, ntiles = (no + BN - 1) / BN;
   const size_t lds = (size_t)8 * HSLOTS * 16;
   auto* kern = &gemm_dma_kernel<kATr, kBTr, OutT, kRagged, WN>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (attr != hipSuccess) return attr;
+  static LdsOf of;
+  if (hipError_t e = of.allow(reinterpret_cast<const void*>(kern), (int)lds)) return e;
   hipLaunchKernelGGL(kern, dim3(mtiles * ntiles), dim3(128 * WN), lds, stream, a, lda, b, ldb, c, mo, no, r,
                      mtiles, ntiles);
   return hipGetLastError();

@@ -72,8 +72,7 @@ Range range(const void* p, uint64_t bytes, const char* name) {
 }
 
 // Device check, cached per device ordinal: the current device must be gfx950.
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_device_state[kMaxDevices];  // 0 unknown, 1 ok, 2 bad
+std::atomic<int> g_device_state[kaio::kMaxDevices];  // 0 unknown, 1 ok, 2 bad
 
 kaio_status check_device(const char* op) {
   int dev = -1;
@@ -81,7 +80,7 @@ kaio_status check_device(const char* op) {
   if (e != hipSuccess || dev < 0)
     return fail(KAIO_ERR_DEVICE, op, "no HIP device available (%s); there is no CPU fallback",
                 hipGetErrorString(e));
-  if (dev >= kMaxDevices) return fail(KAIO_ERR_DEVICE, op, "device ordinal %d out of range", dev);
+  if (dev >= kaio::kMaxDevices) return fail(KAIO_ERR_DEVICE, op, "device ordinal %d out of range", dev);
   int st = g_device_state[dev].load(std::memory_order_acquire);
   if (st == 0) {
     hipDeviceProp_t prop;

@@ -6,10 +6,31 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kaio.h"
 #include "paged.hpp"
 
 namespace kaio {
+
+constexpr int kMaxDevices = 64;
+
+// What a kernel that takes more than 64 KiB of LDS needs once on each device before it is launched there (one static object
+// per kernel).
+class LdsOf {
+  std::atomic<uint64_t> done_{0};   // devices, as bits
+
+ public:
+  hipError_t allow(const void* kern, int bytes) {
+    int device = 0;
+    if (hipError_t e = hipGetDevice(&device)) return e;
+    const uint64_t bit = 1ull << (device & (kMaxDevices - 1));
+    if (done_.load(std::memory_order_acquire) & bit) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 struct QkvProblem {
   const uint16_t* x;        // f16 [m, k]

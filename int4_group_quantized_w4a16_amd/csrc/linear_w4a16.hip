@@ -57,9 +57,8 @@ hipError_t launch_tile(const LinearProblem& p, hipStream_t stream) {
   const uint32_t mtiles = (p.m + BM - 1) / BM, ntiles = (p.n + BN - 1) / BN;
   const size_t lds = (size_t)KS * SetRing<4, WAVES, 1, BM, KS, NQ>::kSize * 16;
   auto* kern = &linear_tile_kernel<WAVES, kAligned, BM, KS, NQ>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (attr != hipSuccess) return attr;
+  static LdsOf of;
+  if (hipError_t e = of.allow(reinterpret_cast<const void*>(kern), (int)lds)) return e;
   hipLaunchKernelGGL(kern, dim3(mtiles * ntiles), dim3(KS * WAVES * 64), lds, stream, p, mtiles);
   return hipGetLastError();
 }

@@ -546,9 +546,8 @@ hipError_t launch_tile_form(const Linear8& p, hipStream_t stream) {
   // as many workgroups as the compute units hold at a time
   const uint64_t tiles = (uint64_t)ctiles * ttiles, most = KS > 1 ? tiles : (160u << 10) / lds * kComputeUnits;
   auto* kern = &linear8_tile_kernel<kRagged, BC, BT, NWC, NWT, KS, kRing>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (attr != hipSuccess) return attr;
+  static LdsOf of;
+  if (hipError_t e = of.allow(reinterpret_cast<const void*>(kern), (int)lds)) return e;
   hipLaunchKernelGGL(kern, dim3((uint32_t)(tiles < most ? tiles : most)), dim3(64 * NWC * NWT * KS), lds, stream, p, ctiles, ttiles);
   return hipGetLastError();
 }
@@ -560,20 +559,14 @@ hipError_t launch_tile(const Linear8& p, hipStream_t stream) {
 template <bool kRounds, int WAVES, int kAhead>
 hipError_t launch_strip(const Linear8& p, hipStream_t stream) {
   const size_t lds = kRounds ? (size_t)p.m * ((p.k + 127) / 128 * 128 + 16) : 0;
-  auto go = [&](auto* kern, const hipError_t attr) {
-    if (attr != hipSuccess) return attr;
+  constexpr int most = (int)(kLinear8Round + 8 * (128 + 16));
+  auto go = [&](auto* kern, LdsOf& of) {
+    if (hipError_t e = of.allow(reinterpret_cast<const void*>(kern), most)) return e;
     hipLaunchKernelGGL(kern, dim3((p.n + 15) / 16), dim3(64 * WAVES), lds, stream, p);
     return hipGetLastError();
   };
-  constexpr int most = (int)(kLinear8Round + 8 * (128 + 16));
-  if (p.bf16) {
-    auto* kern = &linear8_strip_kernel<kRounds, true, WAVES, kAhead>;
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, most);
-    return go(kern, attr);
-  }
-  auto* kern = &linear8_strip_kernel<kRounds, false, WAVES, kAhead>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, most);
-  return go(kern, attr);
+  static LdsOf bf16, f16;
+  return p.bf16 ? go(&linear8_strip_kernel<kRounds, true, WAVES, kAhead>, bf16) : go(&linear8_strip_kernel<kRounds, false, WAVES, kAhead>, f16);
 }
 
 hipError_t launch_form(const Linear8& p, Linear8Form f, hipStream_t stream) {

@@ -661,9 +661,8 @@ hipError_t launch_moe_w4a16(const Moe& p, hipStream_t stream) {
   else hipLaunchKernelGGL(moe_up_kernel<4>, dim3(wgs, blocks), dim3(4 * 64), 0, stream, p);
   if (hipError_t e = hipGetLastError()) return e;
   const uint32_t tokens = p.tokens < kBlock ? p.tokens : kBlock;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_down_kernel),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kDownWaves * kBlock * N * 4);
-  if (attr != hipSuccess) return attr;
+  static LdsOf of;
+  if (hipError_t e = of.allow(reinterpret_cast<const void*>(&moe_down_kernel), kDownWaves * kBlock * N * 4)) return e;
   hipLaunchKernelGGL(moe_down_kernel, dim3(p.hidden / N * p.splits, blocks), dim3(kDownWaves * 64), kDownWaves * tokens * N * 4, stream, p);
   return hipGetLastError();
 }

@@ -60,9 +60,8 @@ hipError_t launch_variant(const QkvProblem& p, hipStream_t stream) {
   const size_t lds = (size_t)KS * SetRing<BITS, WAVES, XDIST, BM, KS, NQ>::kSize * 16;
   const dim3 grid(mtiles * ntiles * (NQ == 1 ? 3 : 1)), block(KS * WAVES * 64);
   auto* kern = &qkv_prefill_kernel<BITS, WAVES, XDIST, kAligned, BM, KS, NQ>;
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (attr != hipSuccess) return attr;
+  static LdsOf of;
+  if (hipError_t e = of.allow(reinterpret_cast<const void*>(kern), (int)lds)) return e;
   hipLaunchKernelGGL(kern, grid, block, lds, stream, p, mtiles);
   return hipGetLastError();
 }

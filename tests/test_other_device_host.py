@@ -1,11 +1,17 @@
 """Tensors on another device than the current one: the C library launches on the current device, so it is called with theirs
-current.  (No GPU: fakes stand for the library and the devices.)"""
+current, and kernels are allowed their LDS on each device once.  (No GPU: fakes stand for the library and the devices.)"""
 import contextlib
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import int4_group_quantized_w4a16_amd as kaio
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 
 
 class FakeLibrary:
@@ -72,3 +78,41 @@ def calls():
 def test_the_library_is_called_on_the_tensors_device(library, name):
     calls()[name]()
     assert library.seen == [(name, torch.device("cpu"))] and library.current == [3]
+
+
+PROGRAM = r"""
+#include <hip/hip_runtime.h>
+static int device = 0, sets = 0;
+static hipError_t next_result = hipSuccess;
+static hipError_t fake_get(int* d) { *d = device; return hipSuccess; }
+static hipError_t fake_set(const void*, hipFuncAttribute, int) { ++sets; return next_result; }
+#define hipGetDevice fake_get
+#define hipFuncSetAttribute fake_set
+#include "launch.hpp"
+#include <cstdio>
+int main() {
+  static kaio::LdsOf lds;
+  int n = 0;
+  for (int d : {0, 0, 1, 0, 1, 63, 63, 5}) {   // once on each
+    device = d;
+    if (lds.allow(nullptr, 100000) != hipSuccess) return 1;
+  }
+  n = sets;
+  device = 7;
+  next_result = hipErrorInvalidValue;          // an error is told, and not taken for done
+  if (lds.allow(nullptr, 100000) != hipErrorInvalidValue) return 2;
+  next_result = hipSuccess;
+  if (lds.allow(nullptr, 100000) != hipSuccess) return 3;
+  printf("%d %d\n", n, sets - n);
+}
+"""
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc is needed")
+def test_lds_is_allowed_on_each_device_once(tmp_path):
+    (tmp_path / "lds.cpp").write_text(PROGRAM)
+    exe = str(tmp_path / "lds")
+    subprocess.run([HIPCC, "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-I", os.path.join(ROOT, "include"), "-I",
+                    os.path.join(ROOT, "int4_group_quantized_w4a16_amd", "csrc"), str(tmp_path / "lds.cpp"), "-o", exe],
+                   check=True, capture_output=True)
+    assert subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split() == ["4", "2"]
