@@ -404,6 +404,11 @@ def _scratch(need, workspace, device, stream):
     return _allocate(device, stream, lambda: torch.empty((need,), dtype=torch.uint8, device=device)) if need else None
 
 
+def _aligned(t, device, stream):
+    """t, or a copy of it where it begins (a slice of a larger tensor) off the 16 bytes that the C library asks for."""
+    return t if t is None or t.data_ptr() % 16 == 0 else _allocate(device, stream, t.clone)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -412,7 +417,8 @@ def kaio_quantize_rows(x, q=None, scale=None, stream=None):
     """Rows rounded to 8 bits; returns (q int8[M, K], scale f32[M]).
 
     x f16 or bf16 [M, K], K a multiple of 16: scale = max |row| / 127, q = round(127 x / max |row|), ties to even.  A row
-    with an infinity or a NaN has scale NaN and q 0.
+    with an infinity or a NaN has scale NaN and q 0.  ``scale`` may begin anywhere in a larger tensor (off 16 bytes the
+    scales are copied there).
     """
     fast = _fast or _quick()
     if fast and stream is None:
@@ -433,8 +439,17 @@ def kaio_quantize_rows(x, q=None, scale=None, stream=None):
     _like(scale, "scale", (torch.float32,), dev, (M,))
     if max(M, K) >= 2 ** 32:
         raise ValueError("dimension exceeds u32")
-    _call(dev, lib().kaio_quantize_rows, 2 if x.dtype == torch.float16 else 1, x.data_ptr(), q.data_ptr(), scale.data_ptr(),
+    # scales of some rows of a larger tensor may begin anywhere: made elsewhere and copied
+    made = scale
+    if scale.data_ptr() % 16:
+        begin, end = scale.data_ptr(), scale.data_ptr() + 4 * M
+        if any(t.data_ptr() < end and begin < t.data_ptr() + t.numel() * t.element_size() for t in (x, q)):
+            raise ValueError("output scale overlaps x or q")
+        made = _allocate(dev, stream, lambda: torch.empty_like(scale))
+    _call(dev, lib().kaio_quantize_rows, 2 if x.dtype == torch.float16 else 1, x.data_ptr(), q.data_ptr(), made.data_ptr(),
           M, K, _stream(dev, stream))
+    if made is not scale:
+        _allocate(dev, stream, lambda: scale.copy_(made))
     return q, scale
 
 
@@ -443,7 +458,8 @@ def kaio_linear_w8a8(x, w, w_scale, x_scale=None, bias=None, activation="none", 
     """y = act(x_scale * w_scale * (x . w^T) + bias) + residual, summed in integers, one rounding; returns y [M, N].
 
     w int8 [N, K] with w_scale f32 [N], K a multiple of 16.  x int8 [M, K] with x_scale f32 [M], or f16 or bf16 [M, K]
-    without, then rounded here as by kaio_quantize_rows.  y, bias [N] and residual [M, N] are in x's dtype; for int8 x in
+    without, then rounded here as by kaio_quantize_rows.  Scales and bias may begin anywhere in a larger tensor (off 16
+    bytes they are copied first).  y, bias [N] and residual [M, N] are in x's dtype; for int8 x in
     ``dtype``, else the dtype of y, residual or bias, the first that is given, else f16.  ``y`` may be ``residual`` itself
     (updated in place).  ``workspace`` (uint8) is allocated here when it is needed and not given.
     """
@@ -485,6 +501,7 @@ def kaio_linear_w8a8(x, w, w_scale, x_scale=None, bias=None, activation="none", 
     _like(y, "y", (dtype,), dev, (M, N))
     if max(M, N, K) >= 2 ** 32:
         raise ValueError("dimension exceeds u32")
+    x_scale, w_scale, bias = (_aligned(t, dev, stream) for t in (x_scale, w_scale, bias))
     need = lib().kaio_linear_w8a8_workspace_size(M, N, K, int(x_scale is not None))
     workspace = _scratch(need, workspace, dev, stream)
     _call(dev, lib().kaio_linear_w8a8, 2 if dtype == torch.float16 else 1, x.data_ptr(), _ptr(x_scale), w.data_ptr(),
