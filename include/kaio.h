@@ -392,8 +392,9 @@ typedef struct kaio_experts {
  * same on every run.  (Blocks of 64 tokens some of whose h are, 32 columns'
  * largest, 4096 or more, or under 2^-16 but not zero, take longer.)
  *
- * Made for few tokens: the chosen experts' weights are read once for each 64
- * tokens.  More are computed as rightly, 64 at a time.
+ * Made for few tokens: of each 64 tokens, a chosen expert's weights are read
+ * once for every 16 of those that chose it, in most cases once.  More tokens
+ * are computed as rightly, 64 at a time.
  *
  * Validation order: e null -> INVALID_ARGUMENT; group_size, activation, experts
  * > 512 or top_k > 16 -> UNSUPPORTED; hidden or inner zero or no multiple of

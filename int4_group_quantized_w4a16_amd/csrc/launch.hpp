@@ -255,7 +255,7 @@ constexpr uint64_t linear8_workspace(uint64_t m, uint64_t k) { return linear8_ro
 // Forms of the 8-bit product: strips of 16 channels by their waves (up to 16 tokens), tiles of channels x tokens.
 enum Linear8Form { kStrip16, kStrip4, kTile32x32, kTile32x64, kTile64x32, kTile64x64, kTile64x128, kTile128x128, kTile128x256, kTile256x256 };
 // Of a tile form the time (0.1 us at k = 4096, n = 4096, weights from HBM) of one workgroup on every compute unit, and of
-// two at once where they fit (0: they do not).  A form's tiles fill the compute units layer by layer, and a layer takes its
+// two at once where they fit (0: they do not).  Other k are not measured, and the choice does not look at k.  A form's tiles fill the compute units layer by layer, and a layer takes its
 // time however many tiles it has: us at n = 4096 by m = 64 / 96 / 128 / 256 / 384 / 509 / 1024 / 2048: 32x32 8.2 11.3 11.3, 32x64 10.4
 // 9.7 10.4 18.5, 64x64 12.6 12.2 12.6 12.8 18.2 18.9, 64x128 - - - 16.4 16.4 16.5 29.4, 128x128 - - - 20.8 20.8 20.8 21.1
 // 39.9, 128x256 - - - - - - 29.2 33.8, 256x256 - - - - - - - 50.6 (57 of six at 8192 x 12288, 128x256 67.6 there).
@@ -287,9 +287,10 @@ constexpr Linear8Form linear8_form(uint32_t m, uint32_t n) {
   return best;
 }
 // Whether a call rounds its 16-bit x in the product's own workgroups, every one all of it, instead of by a launch of its own:
-// us, inside / apart, at m = 1, 4, 8, 16: n 2048, k 2048 5.7 / 5.9, 5.8 / 6.1, 6.3 / 6.5, 7.6 / 6.7; n 4096, k 4096 8.0 / 9.4, 8.5 /
-// 9.7, 9.6 / 9.9, 12.6 / 10.9; n 4096, k 8192 11.4 / 13.6, 13.1 / 14.2, 16.0 / 14.4.  With more than one workgroup for each
-// compute unit it is the other way: n 8192, k 4096 14.0 / 12.7, 15.2 / 13.0, 17.5 / 14.5; 11004 channels 24.4 / 14.7.
+// us of calls one after the other, weights from HBM, inside / apart, at m = 1, 4, 8: n 2048, k 2048 4.9 / 8.6, 5.2 / 8.8, 5.5 / 8.9;
+// n 4096, k 4096 6.7 / 10.4, 7.4 / 10.7, 8.8 / 10.6; n 4096, k 8192 10.1 / 13.3, 11.8 / 13.8.  The limit of one workgroup for
+// each compute unit is that of an earlier form, which was slower past it (11004 channels 24.4 / 14.7); of this one 8192
+// channels, k 4096, take 9.0 / 13.7, 10.1 / 14.1, 12.0 / 14.1.
 constexpr uint32_t kLinear8Round = 1u << 15;   // elements of x that they take
 constexpr bool linear8_rounds(uint32_t m, uint32_t n, uint32_t k) {
   return m <= 8 && n <= 16 * kComputeUnits && (uint64_t)m * k <= kLinear8Round;

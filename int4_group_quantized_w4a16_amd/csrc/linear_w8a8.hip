@@ -22,9 +22,11 @@
 // 12288 by the power that the card allows them (2.4 to 2.5e15 operations/s in
 // long runs; MFMAs alone without loads reach 3.0 to 3.4e15).  In between a
 // compute unit waits for its own blocks.  Measured (16-bit x, rounding included;
-// m x n x k): 1 x 4096 x 4096 6.2 us (2.7 TB/s), 61 x 11004 x 4096 14.1 (3.3
-// TB/s), 509 x 4096 x 4096 22.7, of which rounding 5, 2048 x 4096 x 8192 77, of
-// which rounding 10 (tiles 2.0e15 operations/s), 8192 x 12288 x 4096 325.
+// m x n x k; weights from HBM, in brackets where the 256 MB cache before it keeps
+// them): 1 x 4096 x 4096 6.7 us (6.2), 1 x 4096 x 8192 10.1, 1 x 11004 x 4096 15.6,
+// 61 x 11004 x 4096 19.6 (14.1), 64 x 512 x 8192 12.5, 509 x 4096 x 4096 26 (22 to
+// 23.4), of which rounding 5, 2048 x 4096 x 8192 (77 to 81), of which rounding 10
+// (tiles 2.0e15 operations/s), 8192 x 12288 x 4096 (319 to 346, by box).
 //
 // Results leave by nontemporal stores (plain ones: 413 instead of 381 us for the
 // last of these, in an earlier form), so that they push no operands out of the L2.

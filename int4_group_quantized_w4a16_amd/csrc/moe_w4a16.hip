@@ -5,9 +5,13 @@
 //   y[t] = sum_e p[t, e] ( act(x[t] . G_e) * (x[t] . U_e) ) . D_e + r[t]
 //
 // Four launches: scores, routes, up, down, in blocks of 64 tokens.  With few
-// tokens the chosen experts' weights are the work, each read once per block:
-// 0.516 bytes a weight, against 2 operations for each of an expert's rows, 1 to
-// 16 of them, so that the bound is memory throughout.
+// tokens the chosen experts' weights are the work, 0.516 bytes each against 2
+// operations for each of an expert's rows.  A block's tokens that chose an expert
+// are taken 16 at a time, and its weights are read again for each 16 (the down
+// product: 8 and 16), from the caches where they fit: mostly once with many
+// experts; 64 tokens evenly over 8 experts, top 2, 1.4 times on average, over 4,
+// top 4, four times.  One token is bound by latency, more by memory and the
+// unpacking of the weights.
 //
 // * scores: f64 sums of exact products, so that the order of experts is the
 //   formula's wherever f64 tells them apart; a workgroup takes one expert and
@@ -29,11 +33,13 @@
 //   arrive adds them in order: no sum depends on who came first.
 //
 // Measured, in us, scores + routes + up + down; E experts of I inner and H hidden
-// columns, the active ones' weights over the last two: 1 token, E 64, top 8, I
-// 1024, H 2048: 3 + 3 + 8 + 8 (latency: one wait for memory each).  8 tokens, E 8,
-// top 2, I 8192, H 4096: 5 + 5 + 54 + 40 (374 MB, 4.0 TB/s).  33 tokens, E 128, top
-// 8, I 768, H 2048: 6 + 8 + 42 + 30 (274 MB, 3.8 TB/s).  64 tokens, E 60, top 4, I
-// 1408, H 2048: 5 + 6 + 41 + 34 (262 MB, 3.5 TB/s).  A copy reaches 5.2 TB/s.
+// columns, the active ones' weights over the last two, from HBM but for the first:
+// 1 token, E 64, top 8, I 1024, H 2048: 3 + 3 + 8 + 9 (latency: one wait for memory
+// each).  8 tokens, E 8, top 2, I 8192, H 4096: 5 + 5 + 53 + 40 (374 MB, 4.0 TB/s).
+// 33 tokens, E 128, top 8, I 768, H 2048: 6 + 9 + 42 + 31 (274 MB, 3.8 TB/s).  64
+// tokens, E 60, top 4, I 1408, H 2048: 6 + 7 + 42 + 34 to 38 (262 MB, 3.3 to 3.5 TB/s).
+// 64 tokens of I 4096, H 2048: E 8, top 2 70 in all, E 4, top 4 91; I 2048, E 16, top 8
+// 112.  512 tokens of E 16, top 2, I 1024, H 1024: 76.  A copy reaches 5.2 TB/s.
 
 #include "attention_common.hpp"
 #include "common.hpp"
@@ -242,8 +248,8 @@ __global__ void __launch_bounds__(1024) moe_routes_kernel(Moe p) {
 }
 
 // ---- products ---------------------------------------------------------------
-// Workgroups take strips of kMoeStrip columns (64 to a strip: 50 instead of 43 us for the up product of 33 tokens and 128
-// experts, with half as many waves resident).  A lane holds two words of each of a group's four 32-k steps: row (lane / 16)
+// Workgroups take strips of kMoeStrip columns (64 to a strip: 50 instead of 43 us for an earlier up product of 33 tokens and
+// 128 experts, now 42, with half as many waves resident).  A lane holds two words of each of a group's four 32-k steps: row (lane / 16)
 // of the step's four, columns 2 (lane % 16) and the next; word i is then the B operand of the MFMA whose column c stands for
 // column 2 c + i.  Rows are 16 at a time (32: 6 to 10% less where every expert has more than 16, 20% more elsewhere).
 constexpr int C = 2;
@@ -411,9 +417,10 @@ __global__ void __launch_bounds__(WAVES * 64, 4) moe_up_kernel(Moe p) {
 }
 
 // Units (a group's weights and rows) on the way to a wave of the down product, one after the other into the same registers:
-// copied from register to register, a unit is waited for as soon as it is asked for (31.3 us instead of 30.0 for 33 tokens of
-// 128 experts).  In the up product, with two matrices' weights for each of x's rows, the copies cost less than the loads gain by
-// being sent before the product instead of after it (41 us, 49 in turns).
+// copied from register to register, a unit is waited for as soon as it is asked for (33 tokens of 128 experts with h in f16:
+// 31.3 us instead of 30.0).  In the up product, with two matrices' weights for each of x's rows, the copies cost less than the
+// loads gain by being sent before the product instead of after it (41 us, 49 in turns).  With sixteen rows at a time one unit
+// is on the way: for two there are not the registers (64 tokens of 60 experts: 48 us instead of 34).
 constexpr int kAhead = 3;
 
 struct DownShared {
